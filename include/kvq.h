@@ -57,6 +57,13 @@ typedef enum kvq_status {
     KVQ_ERR_NOMEM = 7         /* device allocation failed (create only) */
 } kvq_status;
 
+/* Element types of kvq_read's rows. */
+enum { KVQ_F16 = 0, KVQ_BF16 = 1, KVQ_F32 = 2 };
+
+/* Blocks per tile of the bounds layout (kvq_block_bounds), and the most blocks a call picks. */
+#define KVQ_BLOCK_TILE 64
+#define KVQ_MAX_BLOCKS 4096
+
 /* Query modes of Eq. 2. */
 enum { KVQ_MODE_SKIP = 0, KVQ_MODE_LOCAL = 1, KVQ_MODE_FULL = 2 };
 
@@ -209,6 +216,102 @@ int kvq_decode_step(const void *q, const void *k, const void *v, const uint8_t *
  */
 int routed_attn_decode_noalloc(const void *q, const kvq_cache *cache, const uint8_t *modes, int w,
                                float *out, kvq_stream_t stream);
+
+/*
+ * kvq_write with the rotary position embedding of the pages' decoder blocks (experimental
+ * setup, model table) applied on the way: k is rotated by its position, then quantized and
+ * appended (Eq. 4); v is appended as it is; q is rotated into q_out.
+ *   q, k, v:   fp16 rows of n_tok tokens, as in kvq_write (q has heads * query_group heads),
+ *              with row strides in ELEMENTS (multiples of 8, at least the row's size), so the
+ *              three may be column ranges of one projection's output. q and q_out may both be
+ *              NULL: keys and values only.
+ *   cos_sin:   fp32 [max_pos][rot_dim]: row t holds the rot_dim/2 cosines of position t, then
+ *              its sines. 16-byte aligned.
+ *   rot_dim:   channels rotated, a multiple of 16 in [16, head_dim]; the others are copied.
+ *   interleaved: 0: channel c is paired with c + rot_dim/2; 1: channel 2c with 2c + 1.
+ *   positions: DEVICE int32 [batch] or NULL: roll each sequence back first, as in
+ *              kvq_decode_step.
+ *   q_out:     fp16 [n_tok][heads * query_group][head_dim], contiguous; may be q itself when
+ *              q_stride is heads * query_group * head_dim.
+ * Token i of sequence s sits at position t = (its KV head's length before the write) + i. A pair
+ * (a, b) becomes (fl(fl(a cos) - fl(b sin)), fl(fl(b cos) + fl(a sin))) in fp32, rounded to
+ * fp16. A write past max_pos is refused like one past the capacity (KVQ_ERR_CAPACITY); the
+ * q_out rows of refused (token, head)s are left as they were. Writes of at most 2 * batch
+ * (and 4096) tokens are one launch and may be captured into a graph; a longer write on a
+ * capturing stream is refused (KVQ_ERR_ARG).
+ */
+int kvq_write_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                   int64_t v_stride, const uint8_t *bits, const int32_t *cu_seqlens, int64_t n_tok,
+                   const float *cos_sin, int64_t max_pos, int rot_dim, int interleaved,
+                   const int32_t *positions, kvq_cache *cache, void *q_out, kvq_stream_t stream);
+
+/*
+ * Read the newest tokens back as plain rows: the last n_s = cu_seqlens[s+1] - cu_seqlens[s]
+ * tokens of each sequence (no counterpart in the paper; for layers that want K and V
+ * themselves, prefix migration, checks).
+ *   cu_seqlens: int32 [batch + 1], as for kvq_write.
+ *   dtype:      KVQ_F16, KVQ_BF16 or KVQ_F32.
+ *   k_out, v_out: [n_rows][heads][head_dim] of that type; one of them may be NULL. Row
+ *               cu_seqlens[s] + i is token len_s - n_s + i: deq = fl(fl(code * s) + z) in fp32 (the
+ *               fp16 value for b = 16), rounded once. A row before the sequence's first
+ *               token is zeros (KVQ_ERR_DEVICE_CHECK); rows from cu_seqlens[batch] on are left
+ *               as they were.
+ */
+int kvq_read(const kvq_cache *cache, const int32_t *cu_seqlens, int64_t n_rows, int dtype,
+             void *k_out, void *v_out, kvq_stream_t stream);
+
+/*
+ * Bounds of blocks of `block` (16, 32, 64 or 128) consecutive keys of each (sequence, KV
+ * head): per channel the minimum and the maximum of deq(k_j) over the block's keys, rounded
+ * to fp16 (no counterpart in the paper: the index that kvq_select_blocks reads).
+ *   cu_seqlens: NULL: every block that holds a key. Else int32 [batch + 1]: only the blocks that
+ *               hold one of the last cu_seqlens[s+1] - cu_seqlens[s] tokens of sequence s (each
+ *               from its first key on): call it with a write's cu_seqlens after the write, and the
+ *               bounds stay those of the whole cache, roll-backs by kvq_cache_truncate included.
+ *   bounds:     fp16 [batch][heads][nt][2][head_dim][64], 16-byte aligned, owned by the
+ *               caller; nt = ceil(ceil(max capacity / block) / 64). Block n of a head is at
+ *               [n / 64][..][..][n % 64]; [0] minima, [1] maxima. Other entries are left as
+ *               they were.
+ */
+int kvq_block_bounds(const kvq_cache *cache, int block, const int32_t *cu_seqlens, void *bounds,
+                     kvq_stream_t stream);
+
+/*
+ * Choose k blocks per (sequence, KV head) for the next decode call (no counterpart in the
+ * paper; a cheaper resolution for its full queries). A block's score is the largest, over
+ * the group's full queries, of sum_c max(q_c lo_c, q_c hi_c): an upper bound of q . k_j over the
+ * block's keys, up to the rounding of the bounds to fp16.
+ *   q:      fp16 [batch][heads * query_group][head_dim].
+ *   bounds: as kvq_block_bounds wrote it for this cache and `block`, current for every key.
+ *   modes:  uint8 [batch][heads * query_group] or NULL (every query full). A KV head without a
+ *           full query gets no blocks.
+ *   k:      1 .. KVQ_MAX_BLOCKS. The first `first` and last `last` blocks of the sequence are
+ *           always chosen (first + last <= k); the others by score, ties to the lower index.
+ *   scores: fp32 [batch][heads][nt][64], 16-byte aligned: every block's score (the sum is
+ *           taken in fp64 and rounded once), -inf past the last block and without a full query.
+ *   ids:    int32 [batch][heads][k]: the chosen blocks in ascending order, then -1.
+ */
+int kvq_select_blocks(const void *q, const kvq_cache *cache, const void *bounds, int block,
+                      const uint8_t *modes, int k, int first, int last, float *scores, int32_t *ids,
+                      kvq_stream_t stream);
+
+/*
+ * Routed decode attention (Eq. 2) with the full queries' keys limited to chosen blocks: as
+ * routed_attn_decode, but a full query of KV head h reads the keys of the blocks in
+ * ids[s][h] that the cache holds (its own key is among them when the last block is listed).
+ *   ids:     int32 [batch][heads][k], 1 <= k <= KVQ_MAX_BLOCKS: ascending, then -1. An entry that is
+ *            not above the one before it, or starts at or past the sequence's length, is passed
+ *            over (KVQ_ERR_DEVICE_CHECK).
+ *   block:   16, 32, 64 or 128; modes, w, out: as routed_attn_decode.
+ *   scratch: DEVICE memory of the caller, 16-byte aligned, used by this call alone until it has
+ *            run; at least routed_attn_decode_blocks_scratch() bytes (0 allows NULL). The scratch
+ *            function returns -1 for arguments the call would refuse.
+ * A query whose blocks hold no key gets zeros.
+ */
+int64_t routed_attn_decode_blocks_scratch(const kvq_cache *cache, int k, int block, int w);
+int routed_attn_decode_blocks(const void *q, const kvq_cache *cache, const int32_t *ids, int k, int block,
+                              const uint8_t *modes, int w, void *scratch, int64_t scratch_bytes,
+                              float *out, kvq_stream_t stream);
 
 /*
  * Read back stored records of one (sequence, head) for tokens first .. first+count-1

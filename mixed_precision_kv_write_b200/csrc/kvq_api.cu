@@ -1,7 +1,8 @@
 // C ABI of the routed mixed-precision KV cache: argument checks, cache allocation,
 // small maintenance kernels (reset, truncate, lengths, export) and the status word.
-// The hot-path kernels live in kvq_write.cu, kvq_decode.cu, kvq_prefill_tc.cu and
-// kvq_route.cu. Every compute entry point is an NVTX range (named after the call) for
+// The hot-path kernels live in kvq_write.cu, kvq_decode.cu, kvq_prefill_tc.cu,
+// kvq_route.cu, kvq_read.cu, kvq_blocks.cu and kvq_blocks_attn.cu. Every compute entry point
+// is an NVTX range (named after the call) for
 // timeline tools; without a tool attached a range costs a few nanoseconds.
 #include <algorithm>
 #include <cstdarg>
@@ -14,7 +15,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
-#include "kvq_internal.cuh"
+#include "kvq_quant.cuh"
 
 namespace {
 
@@ -115,9 +116,25 @@ __global__ void init_side_kernel(float4 *side, int64_t n)
 
 bool valid_cache(const kvq_cache *c) { return c && c->B > 0 && c->H > 0; }
 
+bool on_device(const kvq_cache *c)
+{
+    int dev = -1;
+    return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
+}
+
+uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+bool valid_block(int block) { return block == 16 || block == 32 || block == 64 || block == 128; }
+
 } // namespace
 
 namespace kvq {
+cudaError_t launch_truncate(kvq_cache *c, const int32_t *lengths, cudaStream_t st)
+{
+    const int BH = c->B * c->H;
+    return launch_pdl(truncate_kernel, dim3((BH + 255) / 256), dim3(256), 0, st, c->view, lengths);
+}
+
 namespace {
 cudaEvent_t g_prof_before = nullptr, g_prof_after = nullptr;
 }
@@ -426,9 +443,7 @@ int kvq_cache_truncate(kvq_cache *c, const int32_t *lengths, kvq_stream_t stream
 {
     if (!valid_cache(c)) return fail(KVQ_ERR_ARG, "kvq_cache_truncate: bad cache");
     if (!lengths) return fail(KVQ_ERR_ARG, "kvq_cache_truncate: lengths is NULL");
-    const int BH = c->B * c->H;
-    kvq::launch_pdl(truncate_kernel, dim3((BH + 255) / 256), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream),
-                    c->view, lengths);
+    kvq::launch_truncate(c, lengths, reinterpret_cast<cudaStream_t>(stream));
     cudaError_t e = cudaGetLastError();
     return e ? cuda_fail(e, "kvq_cache_truncate") : ok();
 }
@@ -456,6 +471,132 @@ int kvq_write(const void *k, const void *v, const uint8_t *bits, const int32_t *
     cudaError_t e = kvq::launch_write(c, static_cast<const __half *>(k), static_cast<const __half *>(v),
                                       bits, cu_seqlens, n_tok, reinterpret_cast<cudaStream_t>(stream));
     return e ? cuda_fail(e, "kvq_write") : ok();
+}
+
+int kvq_write_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                   const uint8_t *bits, const int32_t *cu_seqlens, int64_t n_tok, const float *cos_sin,
+                   int64_t max_pos, int rot_dim, int interleaved, const int32_t *positions, kvq_cache *c, void *q_out,
+                   kvq_stream_t stream)
+{
+    const ApiRange range("kvq_write_rope");
+    if (!valid_cache(c)) return fail(KVQ_ERR_ARG, "kvq_write_rope: bad cache");
+    const int64_t kv = (int64_t)c->H * c->D, hq = kv * c->view.G;
+    if (n_tok < 0 || n_tok > (int64_t)INT32_MAX / ((int64_t)c->H * c->view.G))
+        return fail(KVQ_ERR_ARG, "kvq_write_rope: n_tok = %lld out of range", (long long)n_tok);
+    if (rot_dim < 16 || rot_dim > c->D || rot_dim % 16)
+        return fail(KVQ_ERR_ARG, "kvq_write_rope: rot_dim = %d is not a multiple of 16 in [16, head_dim]", rot_dim);
+    if (!cos_sin || max_pos < 1) return fail(KVQ_ERR_ARG, "kvq_write_rope: cos_sin is NULL or max_pos < 1");
+    if (!cu_seqlens) return fail(KVQ_ERR_ARG, "kvq_write_rope: cu_seqlens is NULL");
+    if (n_tok > 0 && (!k || !v || !bits)) return fail(KVQ_ERR_ARG, "kvq_write_rope: k, v or bits is NULL");
+    if ((q == nullptr) != (q_out == nullptr) && n_tok > 0)
+        return fail(KVQ_ERR_ARG, "kvq_write_rope: q and q_out go together");
+    if ((addr(q) | addr(k) | addr(v) | addr(q_out) | addr(cos_sin)) & 15u)
+        return fail(KVQ_ERR_ARG, "kvq_write_rope: q, k, v, q_out and cos_sin must be 16-byte aligned");
+    if (k_stride < kv || v_stride < kv || (q && q_stride < hq) || ((k_stride | v_stride | (q ? q_stride : 0)) & 7))
+        return fail(KVQ_ERR_ARG, "kvq_write_rope: a row stride is below the row's size or not a multiple of 8");
+    if (!on_device(c)) return fail(KVQ_ERR_ARG, "kvq_write_rope: the cache's device is not the current device");
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (!kvq::write_is_short(c, n_tok)) {
+        // a long write's kernels recognise their own call's marks by the call's number, which a
+        // replayed graph would repeat
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(st, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) {
+            cudaGetLastError();
+            return fail(KVQ_ERR_ARG, "kvq_write_rope: only writes of at most 2 * batch tokens can be captured");
+        }
+    }
+    kvq::RopeArgs r;
+    r.q = n_tok > 0 ? static_cast<const __half *>(q) : nullptr;
+    r.q_out = static_cast<__half *>(q_out);
+    r.tab = cos_sin;
+    r.qs = q_stride;
+    r.ks = k_stride;
+    r.vs = v_stride;
+    r.max_pos = max_pos;
+    r.rot = rot_dim;
+    r.interleaved = interleaved != 0;
+    cudaError_t e = kvq::launch_write_rope(c, static_cast<const __half *>(k), static_cast<const __half *>(v), bits,
+                                           cu_seqlens, n_tok, positions, r, st);
+    return e ? cuda_fail(e, "kvq_write_rope") : ok();
+}
+
+int kvq_read(const kvq_cache *c, const int32_t *cu_seqlens, int64_t n_rows, int dtype, void *k_out, void *v_out,
+             kvq_stream_t stream)
+{
+    const ApiRange range("kvq_read");
+    if (!valid_cache(c)) return fail(KVQ_ERR_ARG, "kvq_read: bad cache");
+    if (n_rows < 0 || n_rows > (int64_t)INT32_MAX / c->H)
+        return fail(KVQ_ERR_ARG, "kvq_read: n_rows = %lld out of range", (long long)n_rows);
+    if (dtype != KVQ_F16 && dtype != KVQ_BF16 && dtype != KVQ_F32)
+        return fail(KVQ_ERR_ARG, "kvq_read: dtype = %d is not KVQ_F16, KVQ_BF16 or KVQ_F32", dtype);
+    if (!cu_seqlens) return fail(KVQ_ERR_ARG, "kvq_read: cu_seqlens is NULL");
+    if (n_rows > 0 && !k_out && !v_out) return fail(KVQ_ERR_ARG, "kvq_read: k_out and v_out are both NULL");
+    if ((addr(k_out) | addr(v_out)) & 15u) return fail(KVQ_ERR_ARG, "kvq_read: k_out and v_out must be 16-byte aligned");
+    if (!on_device(c)) return fail(KVQ_ERR_ARG, "kvq_read: the cache's device is not the current device");
+    cudaError_t e = kvq::launch_read(c, cu_seqlens, n_rows, dtype, k_out, v_out, reinterpret_cast<cudaStream_t>(stream));
+    return e ? cuda_fail(e, "kvq_read") : ok();
+}
+
+int kvq_block_bounds(const kvq_cache *c, int block, const int32_t *cu_seqlens, void *bounds, kvq_stream_t stream)
+{
+    const ApiRange range("kvq_block_bounds");
+    if (!valid_cache(c)) return fail(KVQ_ERR_ARG, "kvq_block_bounds: bad cache");
+    if (!valid_block(block)) return fail(KVQ_ERR_ARG, "kvq_block_bounds: block = %d is not 16, 32, 64 or 128", block);
+    if (!bounds || (addr(bounds) & 15u)) return fail(KVQ_ERR_ARG, "kvq_block_bounds: bounds is NULL or not 16-byte aligned");
+    if (!on_device(c)) return fail(KVQ_ERR_ARG, "kvq_block_bounds: the cache's device is not the current device");
+    cudaError_t e = kvq::launch_block_bounds(c, block, cu_seqlens, static_cast<__half *>(bounds),
+                                             reinterpret_cast<cudaStream_t>(stream));
+    return e ? cuda_fail(e, "kvq_block_bounds") : ok();
+}
+
+int kvq_select_blocks(const void *q, const kvq_cache *c, const void *bounds, int block, const uint8_t *modes, int k,
+                      int first, int last, float *scores, int32_t *ids, kvq_stream_t stream)
+{
+    const ApiRange range("kvq_select_blocks");
+    if (!valid_cache(c)) return fail(KVQ_ERR_ARG, "kvq_select_blocks: bad cache");
+    if (!valid_block(block)) return fail(KVQ_ERR_ARG, "kvq_select_blocks: block = %d is not 16, 32, 64 or 128", block);
+    if (k < 1 || k > KVQ_MAX_BLOCKS) return fail(KVQ_ERR_ARG, "kvq_select_blocks: k = %d outside [1, %d]", k, KVQ_MAX_BLOCKS);
+    if (first < 0 || last < 0 || first > k || last > k - first)
+        return fail(KVQ_ERR_ARG, "kvq_select_blocks: first = %d and last = %d do not fit k = %d", first, last, k);
+    if (!q || !bounds || !scores || !ids) return fail(KVQ_ERR_ARG, "kvq_select_blocks: q, bounds, scores or ids is NULL");
+    if ((addr(q) | addr(bounds) | addr(scores)) & 15u || addr(ids) & 3u)
+        return fail(KVQ_ERR_ARG, "kvq_select_blocks: q, bounds and scores must be 16-byte aligned, ids 4-byte aligned");
+    if ((int64_t)c->B * c->H * (((int64_t)c->max_cap + block - 1) / block + 63) / 64 > INT32_MAX / 2)
+        return fail(KVQ_ERR_ARG, "kvq_select_blocks: too many blocks");
+    if (!on_device(c)) return fail(KVQ_ERR_ARG, "kvq_select_blocks: the cache's device is not the current device");
+    cudaError_t e = kvq::launch_select_blocks(static_cast<const __half *>(q), c, static_cast<const __half *>(bounds), block,
+                                              modes, k, first, last, scores, ids, reinterpret_cast<cudaStream_t>(stream));
+    return e ? cuda_fail(e, "kvq_select_blocks") : ok();
+}
+
+int64_t routed_attn_decode_blocks_scratch(const kvq_cache *c, int k, int block, int w)
+{
+    if (!valid_cache(c) || !valid_block(block) || k < 1 || k > KVQ_MAX_BLOCKS || w < 0) return -1;
+    return kvq::decode_blocks_scratch(c, k, block, w);
+}
+
+int routed_attn_decode_blocks(const void *q, const kvq_cache *c, const int32_t *ids, int k, int block,
+                              const uint8_t *modes, int w, void *scratch, int64_t scratch_bytes, float *out,
+                              kvq_stream_t stream)
+{
+    const ApiRange range("routed_attn_decode_blocks");
+    if (!valid_cache(c)) return fail(KVQ_ERR_ARG, "routed_attn_decode_blocks: bad cache");
+    if (!valid_block(block))
+        return fail(KVQ_ERR_ARG, "routed_attn_decode_blocks: block = %d is not 16, 32, 64 or 128", block);
+    if (k < 1 || k > KVQ_MAX_BLOCKS)
+        return fail(KVQ_ERR_ARG, "routed_attn_decode_blocks: k = %d outside [1, %d]", k, KVQ_MAX_BLOCKS);
+    if (w < 0) return fail(KVQ_ERR_ARG, "routed_attn_decode_blocks: w = %d < 0", w);
+    if (!q || !ids || !modes || !out) return fail(KVQ_ERR_ARG, "routed_attn_decode_blocks: q, ids, modes or out is NULL");
+    if ((addr(q) | addr(out) | addr(scratch)) & 15u || addr(ids) & 3u)
+        return fail(KVQ_ERR_ARG, "routed_attn_decode_blocks: q, out and scratch must be 16-byte aligned, ids 4-byte aligned");
+    const int64_t need = kvq::decode_blocks_scratch(c, k, block, w);
+    if (need > 0 && (!scratch || scratch_bytes < need))
+        return fail(KVQ_ERR_ARG, "routed_attn_decode_blocks: scratch of %lld bytes, %lld are needed",
+                    (long long)(scratch ? scratch_bytes : 0), (long long)need);
+    if (!on_device(c)) return fail(KVQ_ERR_ARG, "routed_attn_decode_blocks: the cache's device is not the current device");
+    cudaError_t e = kvq::launch_decode_blocks(static_cast<const __half *>(q), c, ids, k, block, modes, w,
+                                              static_cast<float *>(scratch), out, reinterpret_cast<cudaStream_t>(stream));
+    return e ? cuda_fail(e, "routed_attn_decode_blocks") : ok();
 }
 
 int routed_attn_prefill(const void *q, const kvq_cache *c, const uint8_t *modes, int w,

@@ -374,6 +374,21 @@ cudaError_t launch_route_argmax(const float *za, const float *zb, int64_t n, uin
                                 uint8_t *bits, cudaStream_t st);
 cudaError_t launch_write(kvq_cache *c, const __half *k, const __half *v, const uint8_t *bits,
                          const int32_t *cu, int64_t n_tok, cudaStream_t st);
+// whether a write of n_tok tokens is one launch with no state tied to the call's number
+bool write_is_short(const kvq_cache *c, int64_t n_tok);
+struct RopeArgs;
+cudaError_t launch_write_rope(kvq_cache *c, const __half *k, const __half *v, const uint8_t *bits,
+                              const int32_t *cu, int64_t n_tok, const int32_t *positions, const RopeArgs &r,
+                              cudaStream_t st);
+cudaError_t launch_read(const kvq_cache *c, const int32_t *cu, int64_t n_rows, int dtype, void *k_out, void *v_out,
+                        cudaStream_t st);
+cudaError_t launch_block_bounds(const kvq_cache *c, int block, const int32_t *cu, __half *bounds, cudaStream_t st);
+cudaError_t launch_select_blocks(const __half *q, const kvq_cache *c, const __half *bounds, int block,
+                                 const uint8_t *modes, int k, int first, int last, float *scores, int32_t *ids,
+                                 cudaStream_t st);
+int64_t decode_blocks_scratch(const kvq_cache *c, int k, int block, int w);
+cudaError_t launch_decode_blocks(const __half *q, const kvq_cache *c, const int32_t *ids, int k, int block,
+                                 const uint8_t *modes, int w, float *scratch, float *out, cudaStream_t st);
 cudaError_t launch_decode(const kvq_cache *c, const __half *q, const uint8_t *modes, int w,
                           float *out, cudaStream_t st);
 // one decode step: append the step's tokens (optionally after rolling sequences back to
@@ -384,6 +399,8 @@ cudaError_t launch_decode_step(kvq_cache *c, const __half *q, const __half *k, c
                                cudaStream_t st);
 cudaError_t launch_prefill_tc(const kvq_cache *c, const __half *q, const uint8_t *modes, int w,
                               const int32_t *cu, int64_t n_tok, float *out, cudaStream_t st);
+// rolls sequences back to `lengths` (kvq_cache_truncate)
+cudaError_t launch_truncate(kvq_cache *c, const int32_t *lengths, cudaStream_t st);
 // SM count of the current device (cached per device ordinal)
 int num_sms();
 // Raise `func`'s dynamic shared-memory limit to `bytes` on the current device; done once

@@ -136,6 +136,100 @@ __device__ __forceinline__ void vec_store(const CacheView &c, const uint4 (&raw)
     if (li == 0) reinterpret_cast<float2 *>(&c.side[slot])[part] = make_float2(sc, z);
 }
 
+// ------------------------------------------------------------------ position rotation
+// Rotary position embedding on the way into the cache (the pages' decoder blocks rotate q
+// and k by position). The first `rot` channels of a head form pairs (a, b): channels c and
+// c + rot/2, or neighbours 2c and 2c + 1 when `interleaved`. At position t, with
+// cos/sin = row t of `tab` ([max_pos][rot]: rot/2 cosines, then rot/2 sines):
+//   a' = fl(fl(a cos) - fl(b sin)),  b' = fl(fl(b cos) + fl(a sin))   in fp32, then fp16.
+// Products and sums are rounded one by one (no FMA), so the rotated fp16 rows, and with
+// them the codes, are the same bits whatever kernel or library rotates them this way.
+struct RopeArgs {
+    const __half *q;          // rows to rotate into q_out, or nullptr
+    __half *q_out;            // [n_tok][H * G][D]
+    const float *tab;
+    int64_t qs, ks, vs;       // row strides of q, k, v in elements
+    int64_t max_pos;          // rows of tab
+    int rot, interleaved;
+};
+
+__device__ __forceinline__ float rope_lo(float a, float b, float c, float s)
+{
+    return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+}
+__device__ __forceinline__ float rope_hi(float a, float b, float c, float s)
+{
+    return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+}
+
+__device__ __forceinline__ void rope_load8(const float *p, float (&f)[8])
+{
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(p)), y = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+    f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+}
+
+// Channels c .. c + 7 (x) and c + rot/2 .. (y) of one vector, rotated in place; `row` is
+// the position's row of the table, c a multiple of 8 below rot/2.
+__device__ __forceinline__ void rope_halves(uint4 &x, uint4 &y, const float *row, int c, int rot)
+{
+    float cs[8], sn[8];
+    rope_load8(row + c, cs);
+    rope_load8(row + rot / 2 + c, sn);
+    __half2 *xa = reinterpret_cast<__half2 *>(&x), *yb = reinterpret_cast<__half2 *>(&y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 a = __half22float2(xa[e]), b = __half22float2(yb[e]);
+        xa[e] = __floats2half2_rn(rope_lo(a.x, b.x, cs[2 * e], sn[2 * e]), rope_lo(a.y, b.y, cs[2 * e + 1], sn[2 * e + 1]));
+        yb[e] = __floats2half2_rn(rope_hi(a.x, b.x, cs[2 * e], sn[2 * e]), rope_hi(a.y, b.y, cs[2 * e + 1], sn[2 * e + 1]));
+    }
+}
+
+// Channels c .. c + 7 of one vector as four neighbour pairs, rotated in place.
+__device__ __forceinline__ void rope_pairs(uint4 &x, const float *row, int c, int rot)
+{
+    const float4 cs = __ldg(reinterpret_cast<const float4 *>(row + c / 2));
+    const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + rot / 2 + c / 2));
+    __half2 *xa = reinterpret_cast<__half2 *>(&x);
+    const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 v = __half22float2(xa[e]);
+        xa[e] = __floats2half2_rn(rope_lo(v.x, v.y, cc[e], ss[e]), rope_hi(v.x, v.y, cc[e], ss[e]));
+    }
+}
+
+// A vector spread over D/8 lanes, 8 channels per lane (li = lane's chunk): the lane's chunk
+// after the rotation. Every lane of the warp takes part; `on` says whether this lane's
+// vector is rotated (the same for all its lanes).
+template <int D>
+__device__ __forceinline__ uint4 rope_lane(uint4 x, bool on, const float *row, const RopeArgs &r, int li)
+{
+    constexpr int VL = D / 8;
+    const int c = 8 * li;
+    if (r.interleaved) {
+        if (on && c < r.rot) rope_pairs(x, row, c, r.rot);
+        return x;
+    }
+    const int hc = r.rot / 16;                   // chunks per half
+    const int lane = threadIdx.x & 31, base = lane - li;
+    const int other = li < hc ? li + hc : li < 2 * hc ? li - hc : li;
+    uint4 y;
+    y.x = __shfl_sync(0xffffffffu, x.x, base + other);
+    y.y = __shfl_sync(0xffffffffu, x.y, base + other);
+    y.z = __shfl_sync(0xffffffffu, x.z, base + other);
+    y.w = __shfl_sync(0xffffffffu, x.w, base + other);
+    static_assert(VL <= 32, "a vector lies in one warp");
+    if (on && c < r.rot) {
+        if (li < hc) {
+            rope_halves(x, y, row, c, r.rot);
+        } else {
+            rope_halves(y, x, row, c - r.rot / 2, r.rot);
+        }
+    }
+    return x;
+}
+
 // Per-head results of append_seq, in shared memory (heads beyond kAppendHeads use the
 // cache's arrays in global memory).
 constexpr int kAppendHeads = 64;
@@ -162,11 +256,15 @@ struct AppendShared {
 // and stream ends are committed, visible to the whole block, and (heads below
 // kAppendHeads) also in `as`. Inconsistent cu_seqlens leave the sequence untouched (status
 // set; as.wstart[h] = -1).
-template <int D>
+// ROPE: k and v rows have the strides of `r`, k is rotated by its position before it is
+// quantized, the step's q rows are rotated into r.q_out, and a write past the table's
+// last position is refused like one past the capacity (its q_out rows stay as they were).
+template <int D, bool ROPE = false>
 __device__ __forceinline__ void append_seq(const CacheView &c, const __half *__restrict__ k,
                                            const __half *__restrict__ v, const uint8_t *__restrict__ bits,
                                            const int32_t *__restrict__ cu, int64_t n_tok, uint32_t gen,
-                                           const int32_t *__restrict__ positions, int s, AppendShared &as)
+                                           const int32_t *__restrict__ positions, int s, AppendShared &as,
+                                           const RopeArgs *r = nullptr)
 {
     constexpr int VL = D / 8, VPW = 32 / VL;
     constexpr int kPre = 2;                      // vector passes whose rows are loaded up front
@@ -174,9 +272,14 @@ __device__ __forceinline__ void append_seq(const CacheView &c, const __half *__r
     const int H = c.H;
     const int64_t t0 = cu[s], t1 = cu[s + 1];
     const int roll = positions ? positions[s] : -1;
-    const int cap = c.cap[s];
+    const int cap = ROPE ? (int)min((int64_t)c.cap[s], r->max_pos) : c.cap[s];
     const int64_t sbase = c.slot_base[s];
     const int cpad = c.cap_pad[s];
+    // row i of the call, head h, of K (part 0) or V (part 1)
+    auto row_of = [&](int part, int64_t i, int h) -> const __half * {
+        if (ROPE) return (part ? v + (t0 + i) * r->vs : k + (t0 + i) * r->ks) + (int64_t)h * D;
+        return (part ? v : k) + ((t0 + i) * H + h) * D;
+    };
     if (t0 < 0 || t1 < t0 || t1 > n_tok || (s == 0 && t0 != 0)) {   // block-uniform
         if (tid == 0) set_status(c.status, KVQ_ERR_DEVICE_CHECK);
         for (int h = tid; h < min(H, kAppendHeads); h += blockDim.x) {
@@ -199,7 +302,7 @@ __device__ __forceinline__ void append_seq(const CacheView &c, const __half *__r
         pre[p] = make_uint4(0u, 0u, 0u, 0u);
         if (vi < n_vec) {
             const int pp = vi >> 1;
-            pre[p] = reinterpret_cast<const uint4 *>((vi & 1 ? v : k) + ((t0 + pp / H) * H + pp % H) * D)[li];
+            pre[p] = reinterpret_cast<const uint4 *>(row_of(vi & 1, pp / H, pp % H))[li];
         }
     }
     if (tid == 0) as.bad = 0;
@@ -295,16 +398,37 @@ __device__ __forceinline__ void append_seq(const CacheView &c, const __half *__r
             for (int q = 0; q < kPre; ++q)
                 if (q == p) raw[0] = pre[q];
         } else if (in_range) {
-            raw[0] = reinterpret_cast<const uint4 *>((part ? v : k) + ((t0 + i) * H + h) * D)[li];
+            raw[0] = reinterpret_cast<const uint4 *>(row_of(part, i, h))[li];
+        }
+        int st_rope = -1;
+        if (ROPE) {
+            if (in_range) st_rope = (h < kAppendHeads) ? as.wstart[h] : c.wstart[s * H + h];
+            const bool on = st_rope >= 0 && part == 0;
+            raw[0] = rope_lane<D>(raw[0], on, r->tab + (int64_t)(on ? st_rope + i : 0) * r->rot, *r, li);
         }
         const __half2 mm = vec_minmax<1, VL>(raw);
         if (!in_range) continue;
-        const int st = (h < kAppendHeads) ? as.wstart[h] : c.wstart[s * H + h];
+        const int st = ROPE ? st_rope : (h < kAppendHeads) ? as.wstart[h] : c.wstart[s * H + h];
         if (st < 0) continue;
         const int64_t slot = sbase + (int64_t)h * cpad + st + i;
         const uint32_t meta = meta_on_chip ? as.meta[i * H + h] : c.meta[slot];
         const int b = 2 << (meta & 3u);
         vec_store<1, VL>(c, raw, mm, b, rec_loc(c, s, h, (meta & ~15u) + part * (b * D / 8)), slot, part, li);
+    }
+    if (ROPE && r->q) {                          // the step's queries, D/8 lanes per vector
+        const int HQ = H * c.G;
+        const int64_t n_q = (int64_t)n * HQ;
+        for (int64_t vb = warp * VPW; vb < n_q; vb += 8 * VPW) {
+            const int64_t vi = vb + lane / VL;
+            const int64_t i = vi / HQ;
+            const int hq = (int)(vi % HQ), h = hq / c.G;
+            int st = -1;
+            if (vi < n_q) st = (h < kAppendHeads) ? as.wstart[h] : c.wstart[s * H + h];
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (st >= 0) x = reinterpret_cast<const uint4 *>(r->q + (t0 + i) * r->qs + (int64_t)hq * D)[li];
+            x = rope_lane<D>(x, st >= 0, r->tab + (st >= 0 ? st + i : 0) * r->rot, *r, li);
+            if (st >= 0) reinterpret_cast<uint4 *>(r->q_out + ((t0 + i) * HQ + hq) * D)[li] = x;
+        }
     }
     __syncthreads();
     for (int h = tid; h < H; h += blockDim.x) {  // commit the new lengths and stream ends

@@ -13,6 +13,8 @@
 //                       rint((x - z)/s) in IEEE fp32 round-to-nearest-even (s == 0 -> 0),
 //                       packed LSB-first into the record; (s, z) into the side table;
 //                       commits the new length and stream end of accepted sequences.
+// kvq_write_rope runs the same kernels with the position rotation of q and k in them
+// (write_append_rope_kernel; the scan, then write_quant_rope_kernel).
 // HBM traffic per (token, head): reads 2*D*2 bytes, writes b*D/4 + 16 + 4 bytes.
 #include <algorithm>
 
@@ -25,11 +27,12 @@ namespace {
 // marks the sequence bad for this call, so no head of it is written), checks capacity,
 // and assigns the new tokens' record offsets with a parallel prefix sum of the record
 // sizes b*D/4. The new length/end are committed by the quantize kernel, which sees the
-// per-sequence verdict of every head.
+// per-sequence verdict of every head. max_len: no sequence may grow past it (the rows of
+// the position table of a rotating write; INT32_MAX otherwise).
 template <int TPS, int BS = (TPS < 256 ? 256 : TPS)>
 __global__ void __launch_bounds__(BS)
 write_scan_kernel(CacheView c, const uint8_t *__restrict__ bits, const int32_t *__restrict__ cu,
-                  int64_t n_tok, uint32_t gen)
+                  int64_t n_tok, uint32_t gen, int max_len)
 {
     constexpr int PER = 8;                       // tokens per thread per pass
     constexpr int WARPS = TPS / 32;
@@ -53,7 +56,7 @@ write_scan_kernel(CacheView c, const uint8_t *__restrict__ bits, const int32_t *
     }
     const int n = (int)(t1 - t0);
     const int L0 = c.len[sh];
-    if ((int64_t)L0 + n > c.cap[s]) {
+    if ((int64_t)L0 + n > min(c.cap[s], max_len)) {
         if (tid == 0) {
             set_status(c.status, KVQ_ERR_CAPACITY);
             c.wstart[sh] = -1;
@@ -158,7 +161,7 @@ __device__ __forceinline__ uint64_t ld_relaxed_u64(const uint64_t *p)
 
 __global__ void __launch_bounds__(kScanChunkThreads)
 write_scan_chunk_kernel(CacheView c, const uint8_t *__restrict__ bits, const int32_t *__restrict__ cu,
-                        int64_t n_tok, uint32_t gen, uint64_t *__restrict__ flags, int n_chunks)
+                        int64_t n_tok, uint32_t gen, uint64_t *__restrict__ flags, int n_chunks, int max_len)
 {
     __shared__ uint32_t wsum[kScanChunkThreads / 32], wpre_sh[kScanChunkThreads / 32];
     __shared__ uint32_t excl_sh;
@@ -173,7 +176,7 @@ write_scan_chunk_kernel(CacheView c, const uint8_t *__restrict__ bits, const int
     // every load that does not depend on the token range goes out with cu
     const int64_t t0 = cu[s], t1 = cu[s + 1];
     const int L0 = c.len[sh];
-    const int cap = c.cap[s];
+    const int cap = min(c.cap[s], max_len);
     const uint32_t off0 = c.end[sh];
     if (t0 < 0 || t1 < t0 || t1 > n_tok || (s == 0 && t0 != 0)) {
         if (ck == 0 && tid == 0) {
@@ -318,7 +321,7 @@ struct WqPair {                          // one (token, head) of the CTA
     uint32_t meta;                       // record offset in the stream | width code
     int32_t s;                           // sequence; -1: not written (rejected write or bad call)
     int32_t h;
-    int32_t pad;
+    int32_t pos;                         // the token's position in its sequence
 };
 
 #ifndef KVQ_WQ_MIXED_SUB
@@ -535,15 +538,98 @@ __device__ __forceinline__ void lane_vector(const CacheView &c, const uint4 *vsr
     if (half == 0) reinterpret_cast<float2 *>(&c.side[slot])[part] = make_float2(sc, z);
 }
 
+// The K rows staged in shared memory (pairs of n_pairs (token, head), D values each) rotated in
+// place, each by its pair's position; refused pairs are left alone. A thread takes a chunk
+// of 8 channels together with its partner chunk, so no value is read after it was changed.
+template <int D>
+__device__ __forceinline__ void rope_staged(__half *sk, const WqPair *pairs, int n_pairs, const RopeArgs &r)
+{
+    const int per = r.interleaved ? r.rot / 8 : r.rot / 16;      // steps per vector
+    for (int t = threadIdx.x; t < n_pairs * per; t += kWqThreads) {
+        const int pi = t / per, ci = t % per;
+        if (pairs[pi].s < 0) continue;
+        const float *row = r.tab + (int64_t)pairs[pi].pos * r.rot;
+        uint4 *vec = reinterpret_cast<uint4 *>(sk + pi * D);
+        uint4 x = vec[ci];
+        if (r.interleaved) {
+            rope_pairs(x, row, 8 * ci, r.rot);
+        } else {
+            uint4 y = vec[ci + per];
+            rope_halves(x, y, row, 8 * ci, r.rot);
+            vec[ci + per] = y;
+        }
+        vec[ci] = x;
+    }
+}
+
+// Query rows of kRopeQPairs (token, KV head) pairs from p0 on, rotated into r.q_out; a row
+// whose token was refused stays as it was.
+constexpr int kRopeQPairs = 64;
+template <int D>
+__device__ __forceinline__ void rope_q_tile(const CacheView &c, const RopeArgs &r, const int32_t *__restrict__ cu,
+                                            int64_t n_tok, uint32_t gen, int64_t p0, int32_t *pos_sh)
+{
+    const int H = c.H, G = c.G;
+    const int n = (int)min((int64_t)kRopeQPairs, n_tok * H - p0);
+    pdl_wait();
+    if (threadIdx.x < n) {
+        const int64_t tk = (p0 + threadIdx.x) / H;
+        const int h = (int)((p0 + threadIdx.x) % H);
+        int lo = 0, hi = c.B;                    // cu[lo] <= tk < cu[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cu[mid] <= tk) lo = mid;
+            else hi = mid;
+        }
+        int pos = -1;
+        if (tk >= cu[lo] && tk < cu[lo + 1] && c.bad[lo] != gen) {
+            const int st = c.wstart[lo * H + h];
+            if (st >= 0) pos = (int)(st + (tk - cu[lo]));
+        }
+        pos_sh[threadIdx.x] = pos;
+    }
+    __syncthreads();
+    // a vector's steps: its rotated chunks (with their partners), then its plain chunks
+    const int rc = r.interleaved ? r.rot / 8 : r.rot / 16;
+    const int per = rc + (D - r.rot) / 8;
+    for (int t = threadIdx.x; t < n * G * per; t += kWqThreads) {
+        const int vi = t / per, ci = t % per;
+        const int pi = vi / G, g = vi % G;
+        const int pos = pos_sh[pi];
+        if (pos < 0) continue;
+        const int64_t tk = (p0 + pi) / H;
+        const int hq = (int)((p0 + pi) % H) * G + g;
+        const uint4 *src = reinterpret_cast<const uint4 *>(r.q + tk * r.qs + (int64_t)hq * D);
+        uint4 *dst = reinterpret_cast<uint4 *>(r.q_out + (tk * H * G + hq) * D);
+        const float *row = r.tab + (int64_t)pos * r.rot;
+        if (ci >= rc) {
+            const int ch = r.rot / 8 + ci - rc;
+            dst[ch] = src[ch];
+        } else if (r.interleaved) {
+            uint4 x = src[ci];
+            rope_pairs(x, row, 8 * ci, r.rot);
+            dst[ci] = x;
+        } else {
+            uint4 x = src[ci], y = src[ci + rc];
+            rope_halves(x, y, row, 8 * ci, r.rot);
+            dst[ci] = x;
+            dst[ci + rc] = y;
+        }
+    }
+}
+
 // One CTA per tile of T tokens x HG heads. Warp 0 starts two bulk copies (the tile's K and
 // V rows are contiguous when HG = H, else one copy per token and tensor); meanwhile every
 // thread resolves the destination of one (token, head): its sequence (binary search of
 // cu_seqlens), the call's verdict, the write start, and the record offset the scan kernel
 // assigned. Then each vector of D values is quantized by one lane from shared memory.
-template <int D>
-__global__ void __launch_bounds__(kWqThreads)
-write_quant_kernel(CacheView c, const __half *__restrict__ k, const __half *__restrict__ v,
-                   const int32_t *__restrict__ cu, int64_t n_tok, uint32_t gen, int T, int HG)
+// ROPE: rows have the strides of `r`; the staged K rows are rotated before they are
+// quantized, and the CTAs from n_tiles on rotate the call's query rows.
+template <int D, bool ROPE>
+__device__ __forceinline__ void write_quant_body(const CacheView &c, const __half *__restrict__ k,
+                                                 const __half *__restrict__ v, const int32_t *__restrict__ cu,
+                                                 int64_t n_tok, uint32_t gen, int T, int HG, const RopeArgs *r,
+                                                 int n_tiles)
 {
     extern __shared__ __align__(128) uint8_t wq_smem[];
     __shared__ uint64_t bar;
@@ -556,6 +642,12 @@ write_quant_kernel(CacheView c, const __half *__restrict__ k, const __half *__re
     // before the first read of what the scan writes (widths verdict, write start, offsets).
     pdl_trigger();
     const int H = c.H;
+    if (ROPE && (int)blockIdx.x >= n_tiles) {
+        if (blockIdx.y == 0)
+            rope_q_tile<D>(c, *r, cu, n_tok, gen, (int64_t)((int)blockIdx.x - n_tiles) * kRopeQPairs,
+                           reinterpret_cast<int32_t *>(pairs));
+        return;
+    }
     const int64_t t0 = (int64_t)blockIdx.x * T;
     const int h0 = blockIdx.y * HG;
     const int Tc = (int)(n_tok - t0 < T ? n_tok - t0 : T);
@@ -572,14 +664,15 @@ write_quant_kernel(CacheView c, const __half *__restrict__ k, const __half *__re
     if (warp == 0) {
         if (lane == 0) mbar_arrive_expect_tx(&bar, 2 * tensor_bytes);
         __syncwarp();
-        if (HGc == H) {
+        const int64_t ks = ROPE ? r->ks : (int64_t)H * D, vs = ROPE ? r->vs : (int64_t)H * D;
+        if (HGc == H && (!ROPE || (ks == (int64_t)H * D && vs == (int64_t)H * D))) {
             if (lane < 2)
                 bulk_g2s(lane ? sv : sk, (lane ? v : k) + t0 * H * D, tensor_bytes, &bar);
         } else {
             for (int i = lane; i < 2 * Tc; i += 32) {
                 const int j = i >> 1;
                 bulk_g2s((i & 1 ? sv : sk) + j * HGc * D,
-                         (i & 1 ? v : k) + ((t0 + j) * H + h0) * D, HGc * D * 2, &bar);
+                         (i & 1 ? v + (t0 + j) * vs : k + (t0 + j) * ks) + (int64_t)h0 * D, HGc * D * 2, &bar);
             }
         }
     }
@@ -606,7 +699,7 @@ write_quant_kernel(CacheView c, const __half *__restrict__ k, const __half *__re
         pr.meta = 0;
         pr.s = -1;
         pr.h = h;
-        pr.pad = 0;
+        pr.pos = 0;
         if (tk < cu[s + 1] && c.bad[s] != gen) {
             const int st = c.wstart[s * H + h];
             if (st >= 0) {
@@ -614,6 +707,7 @@ write_quant_kernel(CacheView c, const __half *__restrict__ k, const __half *__re
                 pr.slot = slot_of(c, s, h, st + t_in_seq);
                 pr.meta = c.meta[pr.slot];
                 pr.s = s;
+                pr.pos = (int32_t)(st + t_in_seq);
                 if (t_in_seq == 0) {          // commit the new length and stream end
                     c.len[s * H + h] = st + (cu[s + 1] - cu[s]);
                     c.end[s * H + h] = c.wend[s * H + h];
@@ -640,6 +734,10 @@ write_quant_kernel(CacheView c, const __half *__restrict__ k, const __half *__re
     }
     __syncthreads();
     if (!mbar_wait(&bar, 0, c.status)) return;
+    if (ROPE) {
+        rope_staged<D>(sk, pairs, Tc * HGc, *r);
+        __syncthreads();
+    }
 
     // LPV adjacent lanes per vector: vector vi is pair order[vi / 2], K (even) or V (odd);
     // the lanes of a warp take consecutive vectors of the width-sorted list
@@ -654,6 +752,23 @@ write_quant_kernel(CacheView c, const __half *__restrict__ k, const __half *__re
         lane_vector<D, LPV>(c, src, b, rec_loc(c, pr.s, pr.h, (pr.meta & ~15u) + part * (b * D / 8)), pr.slot, part,
                             lane & 7, half);
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWqThreads)
+write_quant_kernel(CacheView c, const __half *__restrict__ k, const __half *__restrict__ v,
+                   const int32_t *__restrict__ cu, int64_t n_tok, uint32_t gen, int T, int HG)
+{
+    write_quant_body<D, false>(c, k, v, cu, n_tok, gen, T, HG, nullptr, 0);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWqThreads)
+write_quant_rope_kernel(CacheView c, const __half *__restrict__ k, const __half *__restrict__ v,
+                        const int32_t *__restrict__ cu, int64_t n_tok, uint32_t gen, int T, int HG, RopeArgs r,
+                        int n_tiles)
+{
+    write_quant_body<D, true>(c, k, v, cu, n_tok, gen, T, HG, &r, n_tiles);
 }
 
 // Short appends (decode steps): one CTA of 256 threads per sequence does the scan and the
@@ -671,7 +786,94 @@ write_append_kernel(CacheView c, const __half *__restrict__ k, const __half *__r
     append_seq<D>(c, k, v, bits, cu, n_tok, gen, nullptr, blockIdx.x, as);
 }
 
+template <int D>
+__global__ void __launch_bounds__(256)
+write_append_rope_kernel(CacheView c, const __half *__restrict__ k, const __half *__restrict__ v,
+                         const uint8_t *__restrict__ bits, const int32_t *__restrict__ cu, int64_t n_tok,
+                         uint32_t gen, const int32_t *__restrict__ positions, RopeArgs r)
+{
+    __shared__ AppendShared as;
+    pdl_wait();
+    pdl_trigger();
+    append_seq<D, true>(c, k, v, bits, cu, n_tok, gen, positions, blockIdx.x, as, &r);
+}
+
+// Calls this short are one launch (a CTA per sequence); longer ones scan, then quantize.
+bool short_append(const CacheView &c, int64_t n_tok)
+{
+    return n_tok > 0 && n_tok <= 2 * (int64_t)c.B && n_tok <= 4096;
+}
+
+cudaError_t launch_scan(kvq_cache *cache, const uint8_t *bits, const int32_t *cu, int64_t n_tok, uint32_t gen,
+                        int max_len, cudaStream_t st)
+{
+    const CacheView &c = cache->view;
+    const int64_t groups = (int64_t)c.B * c.H;
+    // a warp per (sequence, head) for short appends (decode steps), a block for long ones
+    if (n_tok <= 64 * (int64_t)c.B) {
+        const int64_t blocks = (groups + 7) / 8;
+        return launch_pdl(write_scan_kernel<32>, dim3((unsigned)blocks), dim3(256), 0, st, c, bits, cu, n_tok, gen,
+                          max_len);
+    }
+    // chunks of 1024 tokens per (sequence, head); no sequence has more chunks than
+    // the cache's largest capacity allows (a longer write fails its capacity check)
+    const int n_chunks = (int)std::max<int64_t>(1, std::min<int64_t>((n_tok + kScanChunk - 1) / kScanChunk,
+                                                                         cache->scan_chunks));
+    return launch_pdl(write_scan_chunk_kernel, dim3((unsigned)(groups * n_chunks)), dim3(kScanChunkThreads), 0, st,
+                      c, bits, cu, n_tok, gen, cache->scan_flags, n_chunks, max_len);
+}
+
+// tiles of T tokens x HG heads, at most kWqHalves values per tensor; one token per
+// tile when the call is too short to give every SM a few tiles
+void quant_tiles(const CacheView &c, int64_t n_tok, int &T, int &HG)
+{
+    HG = std::min(c.H, kWqHalves / c.D);
+    T = std::max(1, kWqHalves / (HG * c.D));
+    if (n_tok < (int64_t)T * 2 * num_sms()) T = 1;
+}
+
 } // namespace
+
+bool write_is_short(const kvq_cache *cache, int64_t n_tok) { return short_append(cache->view, n_tok); }
+
+cudaError_t launch_write_rope(kvq_cache *cache, const __half *k, const __half *v, const uint8_t *bits,
+                              const int32_t *cu, int64_t n_tok, const int32_t *positions, const RopeArgs &r,
+                              cudaStream_t st)
+{
+    const CacheView &c = cache->view;
+    const uint32_t gen = ++cache->write_gen;
+    cudaError_t le;
+    if (short_append(c, n_tok)) {
+        profile_before(st);
+        le = c.D == 128 ? launch_pdl(write_append_rope_kernel<128>, dim3(c.B), dim3(256), 0, st, c, k, v, bits, cu, n_tok,
+                                     gen, positions, r)
+                        : launch_pdl(write_append_rope_kernel<64>, dim3(c.B), dim3(256), 0, st, c, k, v, bits, cu, n_tok,
+                                     gen, positions, r);
+        profile_after(st);
+        return le != cudaSuccess ? le : cudaGetLastError();
+    }
+    if (positions && (le = launch_truncate(cache, positions, st)) != cudaSuccess) return le;
+    if (n_tok == 0) return cudaSuccess;
+    profile_before(st);
+    if ((le = launch_scan(cache, bits, cu, n_tok, gen, (int)std::min<int64_t>(r.max_pos, INT32_MAX), st)) != cudaSuccess)
+        return le;
+    int T, HG;
+    quant_tiles(c, n_tok, T, HG);
+    const int64_t n_tiles = (n_tok + T - 1) / T;
+    const int64_t q_tiles = r.q ? (n_tok * c.H + kRopeQPairs - 1) / kRopeQPairs : 0;
+    const dim3 grid((unsigned)(n_tiles + q_tiles), (unsigned)((c.H + HG - 1) / HG));
+    const size_t smem = 2 * kWqHalves * sizeof(__half);
+    le = ensure_smem_attr(c.D == 128 ? (const void *)write_quant_rope_kernel<128>
+                                     : (const void *)write_quant_rope_kernel<64>, smem);
+    if (le != cudaSuccess) return le;
+    le = c.D == 128 ? launch_pdl(write_quant_rope_kernel<128>, grid, dim3(kWqThreads), smem, st, c, k, v, cu, n_tok, gen,
+                                 T, HG, r, (int)n_tiles)
+                    : launch_pdl(write_quant_rope_kernel<64>, grid, dim3(kWqThreads), smem, st, c, k, v, cu, n_tok, gen,
+                                 T, HG, r, (int)n_tiles);
+    if (le != cudaSuccess) return le;
+    profile_after(st);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_write(kvq_cache *cache, const __half *k, const __half *v,
                          const uint8_t *bits, const int32_t *cu, int64_t n_tok, cudaStream_t st)
@@ -680,7 +882,7 @@ cudaError_t launch_write(kvq_cache *cache, const __half *k, const __half *v,
     const uint32_t gen = ++cache->write_gen;
     cudaError_t le = cudaSuccess;
     profile_before(st);
-    if (n_tok > 0 && n_tok <= 2 * (int64_t)c.B && n_tok <= 4096) {
+    if (short_append(c, n_tok)) {
         // short append (decode steps): scan and quantize in one launch, a CTA per sequence
         if (c.D == 128)
             le = launch_pdl(write_append_kernel<128>, dim3(c.B), dim3(256), 0, st, c, k, v, bits, cu, n_tok, gen);
@@ -689,28 +891,11 @@ cudaError_t launch_write(kvq_cache *cache, const __half *k, const __half *v,
         profile_after(st);
         return le != cudaSuccess ? le : cudaGetLastError();
     }
-    {
-        const int64_t groups = (int64_t)c.B * c.H;
-        // a warp per (sequence, head) for short appends (decode steps), a block for long ones
-        if (n_tok <= 64 * (int64_t)c.B) {
-            const int64_t blocks = (groups + 7) / 8;
-            le = launch_pdl(write_scan_kernel<32>, dim3((unsigned)blocks), dim3(256), 0, st, c, bits, cu, n_tok, gen);
-        } else {
-            // chunks of 1024 tokens per (sequence, head); no sequence has more chunks than
-            // the cache's largest capacity allows (a longer write fails its capacity check)
-            const int n_chunks = (int)std::max<int64_t>(1, std::min<int64_t>((n_tok + kScanChunk - 1) / kScanChunk,
-                                                                                 cache->scan_chunks));
-            le = launch_pdl(write_scan_chunk_kernel, dim3((unsigned)(groups * n_chunks)), dim3(kScanChunkThreads), 0, st,
-                            c, bits, cu, n_tok, gen, cache->scan_flags, n_chunks);
-        }
-        if (le != cudaSuccess) return le;
-    }
+    le = launch_scan(cache, bits, cu, n_tok, gen, INT32_MAX, st);
+    if (le != cudaSuccess) return le;
     if (n_tok > 0) {
-        // tiles of T tokens x HG heads, at most kWqHalves values per tensor; one token per
-        // tile when the call is too short to give every SM a few tiles
-        const int HG = std::min(c.H, kWqHalves / c.D);
-        int T = std::max(1, kWqHalves / (HG * c.D));
-        if (n_tok < (int64_t)T * 2 * num_sms()) T = 1;
+        int T, HG;
+        quant_tiles(c, n_tok, T, HG);
         const dim3 grid((unsigned)((n_tok + T - 1) / T), (unsigned)((c.H + HG - 1) / HG));
 
         const size_t smem = 2 * kWqHalves * sizeof(__half);

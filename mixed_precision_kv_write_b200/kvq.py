@@ -7,6 +7,7 @@ missing or a tensor is on the CPU, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -18,14 +19,19 @@ LIB_PATH = os.path.join(_PKG, "libkvq.so")
 KVQ_OK, KVQ_ERR_ARG, KVQ_ERR_BITS, KVQ_ERR_MODE, KVQ_ERR_CAPACITY, KVQ_ERR_CUDA, \
     KVQ_ERR_DEVICE_CHECK, KVQ_ERR_NOMEM = range(8)
 MODE_SKIP, MODE_LOCAL, MODE_FULL = 0, 1, 2
+BLOCK_TILE = 64                  # blocks per tile of the bounds layout
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 # every symbol include/kvq.h declares
 EXPORTS = ("kvq_cache_create", "kvq_cache_create_gqa", "kvq_cache_create_paged", "kvq_cache_destroy", "kvq_cache_reset", "kvq_cache_truncate",
            "kvq_cache_lengths", "kvq_write", "routed_attn_prefill", "routed_attn_decode",
            "routed_attn_decode_noalloc", "kvq_decode_step", "kvq_cache_export", "kvq_check", "kvq_set_profile_events",
+           "kvq_write_rope", "kvq_read", "kvq_block_bounds", "kvq_select_blocks", "routed_attn_decode_blocks",
+           "routed_attn_decode_blocks_scratch",
            "kvq_route_argmax", "kvq_test_fail_alloc", "kvq_test_bounded_wait", "kvq_last_error")
 
 _lib = None
+_HERE = contextlib.nullcontext()
 
 
 class KVQError(RuntimeError):
@@ -61,6 +67,12 @@ def load_library(path: str = LIB_PATH):
         "kvq_check": ([vp, vp], i32),
         "kvq_set_profile_events": ([vp, vp], i32),
         "kvq_route_argmax": ([vp, vp, i64, vp, vp, vp], i32),
+        "kvq_write_rope": ([vp, i64, vp, i64, vp, i64, vp, vp, i64, vp, i64, i32, i32, vp, vp, vp, vp], i32),
+        "kvq_read": ([vp, vp, i64, i32, vp, vp, vp], i32),
+        "kvq_block_bounds": ([vp, i32, vp, vp, vp], i32),
+        "kvq_select_blocks": ([vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp], i32),
+        "routed_attn_decode_blocks_scratch": ([vp, i32, i32, i32], i64),
+        "routed_attn_decode_blocks": ([vp, vp, vp, i32, i32, vp, i32, vp, i64, vp, vp], i32),
         "kvq_test_fail_alloc": ([i32], i32),
         "kvq_test_bounded_wait": ([vp, i64, vp], i32),
         "kvq_last_error": ([], ctypes.c_char_p),
@@ -86,6 +98,11 @@ def _stream(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _on(device):
+    """The cache's device as the current one, for the call."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _check(t, name, dtype, device, shape=None):
@@ -261,6 +278,150 @@ def routed_attn_decode_noalloc(q, cache: KVQCache, modes, w: int, out=None, stre
     _check(out, "out", torch.float32, dev, shape)
     _raise(load_library().routed_attn_decode_noalloc(_ptr(q), cache.handle, _ptr(modes), int(w),
                                                      _ptr(out), _stream(stream, dev)))
+    return out
+
+
+def _rows(t, name, heads, head_dim, device, n=None):
+    """Checks fp16 rows [n, heads, head_dim] whose heads are contiguous; returns the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if t.dtype != torch.float16:
+        raise TypeError(f"{name} must be {torch.float16} (got {t.dtype})")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must have shape {(n, heads, head_dim)} (got {tuple(t.shape)})")
+    st = t.stride()
+    if st[2] != 1 or (heads > 1 and st[1] != head_dim):
+        raise ValueError(f"{name}: the heads of a row must be contiguous (strides {st})")
+    return st[0] if t.shape[0] > 1 else max(st[0], heads * head_dim)
+
+
+def kvq_write_rope(q, k, v, bits, cu_seqlens, cache: KVQCache, cos_sin, interleaved: bool = False, positions=None,
+                   q_out=None, stream=None):
+    """Rotate q and k by position, append k and v at widths bits (kvq_write_rope); returns the
+    rotated q [n_tok, HQ, D].
+
+    q [n_tok, HQ, D], k, v [n_tok, H, D]: fp16, row strides free (heads of a row contiguous),
+    q may be None. cos_sin: fp32 [max_pos, rot_dim], row t the cosines of position t, then its
+    sines; rot_dim is its width. positions: int32 [B], roll the sequences back first."""
+    dev, H, D = cache.device, cache.heads, cache.head_dim
+    n = k.shape[0]
+    ks, vs = _rows(k, "k", H, D, dev), _rows(v, "v", H, D, dev, n)
+    qs = 0
+    if q is not None:
+        qs = _rows(q, "q", cache.query_heads, D, dev, n)
+        if q_out is None:
+            q_out = torch.empty((n, cache.query_heads, D), dtype=torch.float16, device=dev)
+        _check(q_out, "q_out", torch.float16, dev, (n, cache.query_heads, D))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check(bits, "bits", torch.uint8, dev, (n, H))
+    _check(cu_seqlens, "cu_seqlens", torch.int32, dev, (cache.batch + 1,))
+    _check(cos_sin, "cos_sin", torch.float32, dev)
+    if cos_sin.dim() != 2:
+        raise ValueError(f"cos_sin must be [max_pos, rot_dim] (got {tuple(cos_sin.shape)})")
+    if positions is not None:
+        _check(positions, "positions", torch.int32, dev, (cache.batch,))
+    with _on(dev):
+        _raise(load_library().kvq_write_rope(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(bits), _ptr(cu_seqlens), n,
+                                             _ptr(cos_sin), cos_sin.shape[0], cos_sin.shape[1], int(interleaved),
+                                             _ptr(positions), cache.handle, _ptr(q_out), _stream(stream, dev)))
+    return q_out
+
+
+def kvq_read(cache: KVQCache, cu_seqlens, n_rows: int, dtype=torch.float16, k_out=None, v_out=None, stream=None):
+    """The last cu_seqlens[s+1] - cu_seqlens[s] tokens of each sequence as K and V rows
+    [n_rows, H, D] of `dtype` (float16, bfloat16, float32); n_rows = cu_seqlens[-1]."""
+    dev = cache.device
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be one of {tuple(_DTYPES)} (got {dtype})")
+    _check(cu_seqlens, "cu_seqlens", torch.int32, dev, (cache.batch + 1,))
+    shape = (int(n_rows), cache.heads, cache.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+    _check(k_out, "k_out", dtype, dev, shape)
+    _check(v_out, "v_out", dtype, dev, shape)
+    with _on(dev):
+        _raise(load_library().kvq_read(cache.handle, _ptr(cu_seqlens), shape[0], _DTYPES[dtype], _ptr(k_out),
+                                       _ptr(v_out), _stream(stream, dev)))
+    return k_out, v_out
+
+
+def block_tiles(cache: KVQCache, block: int) -> int:
+    """Tiles of 64 blocks per (sequence, head) in the bounds of `block`-key blocks."""
+    if block not in (16, 32, 64, 128):
+        raise ValueError(f"block must be 16, 32, 64 or 128 (got {block})")
+    return -(-(-(-max(cache.capacity) // block)) // BLOCK_TILE)
+
+
+def block_bounds(cache: KVQCache, block: int, cu_seqlens=None, out=None, stream=None):
+    """Per block of `block` keys, each channel's minimum and maximum of the dequantized keys
+    (kvq_block_bounds): fp16 [B, H, nt, 2, D, 64]. With cu_seqlens, only the blocks that hold the
+    newest tokens it counts are renewed in `out`; without it, every block."""
+    dev = cache.device
+    shape = (cache.batch, cache.heads, block_tiles(cache, block), 2, cache.head_dim, BLOCK_TILE)
+    if cu_seqlens is not None:
+        _check(cu_seqlens, "cu_seqlens", torch.int32, dev, (cache.batch + 1,))
+        if out is None:
+            raise ValueError("cu_seqlens renews blocks of an `out` that holds the others")
+    if out is None:
+        out = torch.zeros(shape, dtype=torch.float16, device=dev)
+    _check(out, "out", torch.float16, dev, shape)
+    with _on(dev):
+        _raise(load_library().kvq_block_bounds(cache.handle, block, _ptr(cu_seqlens), _ptr(out), _stream(stream, dev)))
+    return out
+
+
+def select_blocks(q, cache: KVQCache, bounds, block: int, k: int, modes=None, first: int = 1, last: int = 1, scores=None,
+                  ids=None, stream=None):
+    """Choose k blocks per (sequence, KV head) for the full queries of q [B, HQ, D]
+    (kvq_select_blocks); returns (ids int32 [B, H, k] ascending then -1, scores fp32
+    [B, H, nt * 64])."""
+    dev, B, H = cache.device, cache.batch, cache.heads
+    nt = block_tiles(cache, block)
+    _check(q, "q", torch.float16, dev, (B, cache.query_heads, cache.head_dim))
+    _check(bounds, "bounds", torch.float16, dev, (B, H, nt, 2, cache.head_dim, BLOCK_TILE))
+    if modes is not None:
+        _check(modes, "modes", torch.uint8, dev, (B, cache.query_heads))
+    if scores is None:
+        scores = torch.empty((B, H, nt * BLOCK_TILE), dtype=torch.float32, device=dev)
+    if ids is None:
+        ids = torch.empty((B, H, k), dtype=torch.int32, device=dev)
+    _check(scores, "scores", torch.float32, dev, (B, H, nt * BLOCK_TILE))
+    _check(ids, "ids", torch.int32, dev, (B, H, k))
+    with _on(dev):
+        _raise(load_library().kvq_select_blocks(_ptr(q), cache.handle, _ptr(bounds), block, _ptr(modes), int(k),
+                                                int(first), int(last), _ptr(scores), _ptr(ids), _stream(stream, dev)))
+    return ids, scores
+
+
+def routed_attn_decode_blocks(q, cache: KVQCache, ids, block: int, modes, w: int, out=None, stream=None):
+    """Routed decode attention (Eq. 2) whose full queries read the blocks of ids [B, H, k]
+    (as select_blocks returns them); q [B, HQ, D] at t = len - 1; returns fp32 out."""
+    dev = cache.device
+    shape = (cache.batch, cache.query_heads, cache.head_dim)
+    _check(q, "q", torch.float16, dev, shape)
+    _check(modes, "modes", torch.uint8, dev, shape[:2])
+    _check(ids, "ids", torch.int32, dev)
+    if ids.dim() != 3 or ids.shape[:2] != (cache.batch, cache.heads):
+        raise ValueError(f"ids must be [{cache.batch}, {cache.heads}, k] (got {tuple(ids.shape)})")
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
+    _check(out, "out", torch.float32, dev, shape)
+    k, lib = ids.shape[2], load_library()
+    need = lib.routed_attn_decode_blocks_scratch(cache.handle, k, block, int(w))
+    with _on(dev):
+        st = torch.cuda.current_stream(dev) if stream is None else stream
+        scratch = None
+        if need > 0:
+            # owned by this call: allocated for the stream that runs it
+            with torch.cuda.stream(st):
+                scratch = torch.empty(need, dtype=torch.uint8, device=dev)
+        _raise(lib.routed_attn_decode_blocks(_ptr(q), cache.handle, _ptr(ids), k, block, _ptr(modes), int(w),
+                                             _ptr(scratch), max(need, 0), _ptr(out), _stream(st, dev)))
     return out
 
 
