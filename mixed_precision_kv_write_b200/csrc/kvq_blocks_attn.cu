@@ -21,16 +21,24 @@
 // for the 128-row tiles of tcgen05 (G is 1 to 64, and the codes would have to be unpacked to
 // shared memory first); the loads, not the products, are what the time goes to.
 //
-// The keys of a tile (up to 256 of a warp's share) are first sorted by width, so that 16 keys
-// of one width unpack by one code path: a 16-bit half of a word holds 16/b codes, one mask
-// turns field i of both halves into the fp16 pair 1024 + 2^(b i) c, one fused multiply-add into
-// c'. For K the two halves are channels of one key (q is stored in the matching order, one
+// The keys of a tile (up to 1024 of a CTA's share) are first sorted by width, so that 16 keys
+// of one width unpack by one code path, and the warps take equal runs of 16-key steps. A
+// 16-bit half of a word holds 16/b codes; one mask-and-or puts field i of both halves into the
+// mantissa of the power of two 2^(10 - b i) whose last place there is 1, the pair 2^(10 - b i) + c,
+// and one addition takes it to c'. For K the two halves are channels of one key (q is stored in the matching order, one
 // order per width); for V they are the same channels of two keys (one byte permutation).
 //
 // Online softmax: the running maximum of a query moves only when a logit exceeds it by
 // more than 8 (log2 units), a warp-uniform branch. The warps of a CTA share a (sequence, KV
-// head) and merge at the end; with more than one CTA per (sequence, KV head) the partial
-// states go to the caller's scratch and a second launch merges them.
+// head) and merge at the end; up to 8 CTAs that share one form a cluster and merge through
+// distributed shared memory; more of them leave partial states in the caller's scratch, which
+// a second launch merges.
+//
+// Latency: the records of a tile are asked for as soon as their offsets are known (bulk
+// prefetches into L2, one per 16 consecutive keys), so the loads of the 16-key steps, which
+// each warp issues one step at a time, find them there.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "kvq_values.cuh"
@@ -38,15 +46,17 @@
 namespace kvq {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kQ = 8;                            // query heads per warp
-constexpr int kTileKeys = 256;                   // keys sorted by width at a time
+constexpr int kSteps = 4;                        // 32-key steps of a warp's part of a tile
+constexpr int kTileKeys = kWarps * kSteps * 32;  // keys sorted by width at a time
 constexpr int kSlots = kTileKeys + 4 * 16;       // each width's keys are padded to 16
 constexpr float kLazy = 8.f;                     // running-max slack, log2 units
 constexpr float kMInit = -1e30f;                 // running max before the first key
+constexpr int kMaxCluster = 8;                   // CTAs of a cluster
 constexpr uint32_t kValid = 4u;                  // meta bit of a real key (bits 0..1: width code)
 
-struct WarpTile {
+struct Tile {
     float4 side[kSlots];                         // (s_K cdot, z'_K cdot, s_V, z'_V), sorted
     uint32_t ent[kSlots];                        // record offset | kValid | width code, sorted
 };
@@ -54,11 +64,15 @@ struct WarpTile {
 template <int D>
 struct Smem {
     union {
-        WarpTile tile[kWarps];
+        Tile tile;
         float o[kWarps][kQ][D + 4];              // the warps' states: o, then m and l
     };
     uint4 q[4][D / 32][32];                      // per width: a lane's query operands, 16 bytes at a time
+    __half rows[kQ][D + 8];                      // the queries
     float qsum[kQ];
+    float done[kQ][D + 4];                       // the CTA's state for the cluster: o, then m and l
+    int cnt[kWarps][4];                          // keys of each width in each warp's part of the tile
+    uint32_t some[4], smax[4];                   // per width: a real key's entry; the largest s_V's bits
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -89,19 +103,17 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-__device__ __forceinline__ uint32_t hfma2u(uint32_t x, uint32_t m, uint32_t a)
+// (field of SHIFT's bits in both halves of p) - 2^(BITS - 1): the field joins the mantissa of
+// 2^(10 - SHIFT), then 2^(10 - SHIFT) + 2^(BITS - 1) is subtracted; every step is exact.
+template <int BITS, int SHIFT>
+__device__ __forceinline__ uint32_t field(uint32_t p)
 {
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&m),
-                              *reinterpret_cast<const __half2 *>(&a));
+    constexpr uint32_t mask = (((1u << BITS) - 1u) << SHIFT) * 0x10001u;
+    constexpr uint32_t magic = (uint32_t)((25 - SHIFT) << 10) * 0x10001u;
+    constexpr uint32_t off = (0x8000u | (uint32_t)((25 - SHIFT) << 10) | (1u << (BITS - 1 + SHIFT))) * 0x10001u;
+    const uint32_t x = (p & mask) | magic, m = off;
+    const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&m));
     return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-// fp16 bits of a power of two 2^e (-14 <= e <= 15), in both halves
-__host__ __device__ constexpr uint32_t pow2h2(int e) { return (uint32_t)((15 + e) << 10) * 0x10001u; }
-// fp16 bits of -(2^e + a), a a small power of two below 2^e (or 0), in both halves
-__host__ __device__ constexpr uint32_t neg_sum_h2(int e, int a)
-{
-    return (0x8000u | (uint32_t)((15 + e) << 10) | (uint32_t)((a << 10) >> e)) * 0x10001u;
 }
 
 // The 16/BITS centred codes in each half of p (LSB-first) as fp16 pairs: x[i] = (field i of
@@ -112,52 +124,76 @@ __device__ __forceinline__ void fields(uint32_t p, uint32_t (&x)[16 / BITS])
     if constexpr (BITS == 16) {
         x[0] = p;
     } else if constexpr (BITS == 8) {
-        // bytes with 0x64 above them: 1024 + c; 1152 = 1024 + 128
-        x[0] = hfma2u(__byte_perm(p, 0x64646464u, 0x4240), pow2h2(0), neg_sum_h2(10, 128));
-        x[1] = hfma2u(__byte_perm(p, 0x64646464u, 0x4341), pow2h2(0), neg_sum_h2(10, 128));
+        x[0] = field<8, 0>(p);
+        x[1] = field<8, 0>(p >> 8);
     } else if constexpr (BITS == 4) {
-        // fields at bits 0 and 4 (after one shift for the upper two): 1024 + 16^i c
         const uint32_t h = p >> 8;
-        x[0] = hfma2u((p & 0x000F000Fu) | 0x64006400u, pow2h2(0), neg_sum_h2(10, 8));
-        x[1] = hfma2u((p & 0x00F000F0u) | 0x64006400u, pow2h2(-4), neg_sum_h2(6, 8));
-        x[2] = hfma2u((h & 0x000F000Fu) | 0x64006400u, pow2h2(0), neg_sum_h2(10, 8));
-        x[3] = hfma2u((h & 0x00F000F0u) | 0x64006400u, pow2h2(-4), neg_sum_h2(6, 8));
+        x[0] = field<4, 0>(p);
+        x[1] = field<4, 4>(p);
+        x[2] = field<4, 0>(h);
+        x[3] = field<4, 4>(h);
     } else {
-        // fields at bits 0 .. 8 (after one shift for the upper three): 1024 + 4^i c
-        const uint32_t h = p >> 10;
-        x[0] = hfma2u((p & 0x00030003u) | 0x64006400u, pow2h2(0), neg_sum_h2(10, 2));
-        x[1] = hfma2u((p & 0x000C000Cu) | 0x64006400u, pow2h2(-2), neg_sum_h2(8, 2));
-        x[2] = hfma2u((p & 0x00300030u) | 0x64006400u, pow2h2(-4), neg_sum_h2(6, 2));
-        x[3] = hfma2u((p & 0x00C000C0u) | 0x64006400u, pow2h2(-6), neg_sum_h2(4, 2));
-        x[4] = hfma2u((p & 0x03000300u) | 0x64006400u, pow2h2(-8), neg_sum_h2(2, 2));
-        x[5] = hfma2u((h & 0x00030003u) | 0x64006400u, pow2h2(0), neg_sum_h2(10, 2));
-        x[6] = hfma2u((h & 0x000C000Cu) | 0x64006400u, pow2h2(-2), neg_sum_h2(8, 2));
-        x[7] = hfma2u((h & 0x00300030u) | 0x64006400u, pow2h2(-4), neg_sum_h2(6, 2));
+        const uint32_t h = p >> 8;
+        x[0] = field<2, 0>(p);
+        x[1] = field<2, 2>(p);
+        x[2] = field<2, 4>(p);
+        x[3] = field<2, 6>(p);
+        x[4] = field<2, 0>(h);
+        x[5] = field<2, 2>(h);
+        x[6] = field<2, 4>(h);
+        x[7] = field<2, 6>(h);
+    }
+}
+
+// Where a stream's bytes are: PAGED as RecLoc::at, else base + offset.
+template <bool PAGED>
+__device__ __forceinline__ const uint8_t *byte_at(const RecLoc &L, uint32_t off)
+{
+    return PAGED ? L.at(off) : L.base + off;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// Bytes [o0, o1) of a stream (multiples of 16) into L2, page by page.
+template <bool PAGED>
+__device__ __forceinline__ void prefetch_records(const RecLoc &L, uint32_t o0, uint32_t o1)
+{
+    if (!PAGED) {
+        prefetch_l2(L.base + o0, o1 - o0);
+        return;
+    }
+    while (o0 < o1) {
+        const uint32_t n = min(o1 - o0, (1u << L.shift) - (o0 & ((1u << L.shift) - 1u)));
+        prefetch_l2(L.at(o0), n);
+        o0 += n;
     }
 }
 
 // BYTES bytes of a record at logical offset `off` of the stream (aligned to min(BYTES, 16), so a
 // 16-byte piece lies in one page) into words; 2 bytes fill the low half of one word.
-template <int BYTES>
+template <int BYTES, bool PAGED>
 __device__ __forceinline__ void load_bytes(const RecLoc &L, uint32_t off, uint32_t (&w)[(BYTES + 3) / 4])
 {
     if constexpr (BYTES >= 16) {
 #pragma unroll
         for (int i = 0; i < BYTES / 16; ++i) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(L.at(off + 16u * i)));
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(byte_at<PAGED>(L, off + 16u * i)));
             w[4 * i] = x.x;
             w[4 * i + 1] = x.y;
             w[4 * i + 2] = x.z;
             w[4 * i + 3] = x.w;
         }
     } else if constexpr (BYTES == 8) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(L.at(off)));
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(byte_at<PAGED>(L, off)));
         w[0] = x.x;
         w[1] = x.y;
     } else if constexpr (BYTES == 4) {
-        w[0] = __ldg(reinterpret_cast<const uint32_t *>(L.at(off)));
+        w[0] = __ldg(reinterpret_cast<const uint32_t *>(byte_at<PAGED>(L, off)));
     } else {
-        w[0] = __ldg(reinterpret_cast<const unsigned short *>(L.at(off)));
+        w[0] = __ldg(reinterpret_cast<const unsigned short *>(byte_at<PAGED>(L, off)));
     }
 }
 
@@ -171,11 +207,12 @@ struct State {
     float unit;
 };
 
-// Keys [0, n) of the sorted tile from slot `base` on, all of width 2 << CLS, 16 at a time.
-template <int D, int CLS>
-__device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const WarpTile &tl, const RecLoc &L, int base, int n,
-                                          float fac, bool on0, bool on1)
+// Slots base .. base + n - 1 of the sorted tile, all of width 2 << CLS, 16 at a time.
+template <int D, int CLS, bool PAGED>
+__device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const RecLoc &L, int base, int n, float fac, bool on0,
+                                          bool on1)
 {
+    const Tile &tl = sm.tile;
     constexpr int BITS = 2 << CLS;
     constexpr int KW = D * BITS / 128;           // words of a lane's D/4 channels of K
     constexpr int VB = D * BITS / 64;            // bytes of a lane's D/8 channels of V
@@ -196,14 +233,14 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
         const uint2 f0 = *reinterpret_cast<const uint2 *>(&tl.ent[c + 2 * t]);
         const uint2 f1 = *reinterpret_cast<const uint2 *>(&tl.ent[c + 8 + 2 * t]);
         uint32_t k0[KW], k1[KW];
-        load_bytes<KW * 4>(L, (e0 & ~15u) + 4 * KW * t, k0);
-        load_bytes<KW * 4>(L, (e1 & ~15u) + 4 * KW * t, k1);
+        load_bytes<KW * 4, PAGED>(L, (e0 & ~15u) + 4 * KW * t, k0);
+        load_bytes<KW * 4, PAGED>(L, (e1 & ~15u) + 4 * KW * t, k1);
         uint32_t v[4][(VB + 3) / 4];
         const uint32_t vo = D * BITS / 8 + VB * g;
-        load_bytes<VB>(L, (f0.x & ~15u) + vo, v[0]);
-        load_bytes<VB>(L, (f0.y & ~15u) + vo, v[1]);
-        load_bytes<VB>(L, (f1.x & ~15u) + vo, v[2]);
-        load_bytes<VB>(L, (f1.y & ~15u) + vo, v[3]);
+        load_bytes<VB, PAGED>(L, (f0.x & ~15u) + vo, v[0]);
+        load_bytes<VB, PAGED>(L, (f0.y & ~15u) + vo, v[1]);
+        load_bytes<VB, PAGED>(L, (f1.x & ~15u) + vo, v[2]);
+        load_bytes<VB, PAGED>(L, (f1.y & ~15u) + vo, v[3]);
         float s[4] = {0.f, 0.f, 0.f, 0.f};
         // a word gives F operand pairs of its key; two of them make one instruction's depth of 16
 #pragma unroll
@@ -306,8 +343,8 @@ struct Job {
     float *part;                                 // [unit][n_split][qs][D + 4]
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 4)
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 2)
 decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *__restrict__ out)
 {
     extern __shared__ __align__(16) uint8_t raw[];
@@ -328,8 +365,8 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         local |= (m == KVQ_MODE_LOCAL ? 1u : 0u) << i;
         if (m > 2 && tid == 0 && split == 0) set_status(c.status, KVQ_ERR_MODE);
     }
-    // the unit's entries: the listed blocks' keys (padded to 32), then the local window's; the
-    // warps of all its CTAs take equal shares
+    // the unit's entries: the listed blocks' keys (padded to 32), then the local window's; its
+    // CTAs take equal shares, multiples of 32
     const int nb = (len + (1 << job.block_shift) - 1) >> job.block_shift;
     const int e_block = full ? ((min(job.k, nb) << job.block_shift) + 31) & ~31 : 0;
     if (full && sub == 0 && split == 0)          // no list of distinct blocks is longer than nb
@@ -337,28 +374,36 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
             if (job.ids[(int64_t)sh * job.k + x] >= 0) set_status(c.status, KVQ_ERR_DEVICE_CHECK);
     const int wl = min(len, (int)min((int64_t)job.w + 1, (int64_t)len));
     const int e_all = e_block + (local ? wl : 0);
-    const int share = ((e_all + job.n_split * kWarps - 1) / (job.n_split * kWarps) + 31) & ~31;
+    const int share = ((e_all + job.n_split - 1) / job.n_split + 31) & ~31;
 
-    // query operands in each width's order, and the sums over channels
+    // the queries, then their operands in each width's order and their sums over channels
+    for (int x = tid; x < kQ * (D / 8); x += kThreads) {
+        const int qi = x / (D / 8), ch = x % (D / 8);
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (qi < nq) v = __ldg(reinterpret_cast<const uint4 *>(q + (q0 + qi) * D) + ch);
+        *reinterpret_cast<uint4 *>(&sm.rows[qi][8 * ch]) = v;
+    }
+    __syncthreads();
+#pragma unroll 1
     for (int x = tid; x < 4 * (D / 32) * 32; x += kThreads) {
         const int cls = x / (D / 32 * 32), i = x / 32 % (D / 32), ln = x % 32;
-        const int qi = ln >> 2, ch0 = (ln & 3) * (D / 4), bits = 2 << cls, f = 16 / bits;
-        uint32_t r[4] = {0u, 0u, 0u, 0u};
-        if (qi < nq) {
+        const int ch0 = (ln & 3) * (D / 4), fl = 3 - cls, f = 1 << fl;     // f = 16 / bits fields per half word
+        uint32_t r[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int p = 4 * i + e;         // operand pair: word p / f, field p % f
-                const __half *src = q + (q0 + qi) * D + ch0 + p / f * (2 * f) + p % f;
-                const __half2 v = __halves2half2(src[0], src[f]);
-                r[e] = *reinterpret_cast<const uint32_t *>(&v);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const int p = 4 * i + e;             // operand pair: word p / f, field p % f
+            const __half *src = &sm.rows[ln >> 2][ch0 + ((p >> fl) << (fl + 1)) + (p & (f - 1))];
+            const __half2 v = __halves2half2(src[0], src[f]);
+            r[e] = *reinterpret_cast<const uint32_t *>(&v);
         }
         sm.q[cls][i][ln] = make_uint4(r[0], r[1], r[2], r[3]);
     }
-    for (int qi = warp; qi < kQ; qi += kWarps) {
+    static_assert(kWarps == kQ, "a warp sums one query");
+    {
+        const int qi = warp;
         float a = 0.f;
-        if (qi < nq)
-            for (int ch = lane; ch < D; ch += 32) a += __half2float(q[(q0 + qi) * D + ch]);
+#pragma unroll
+        for (int ch = 0; ch < D; ch += 32) a += __half2float(sm.rows[qi][ch + lane]);
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
         if (lane == 0) sm.qsum[qi] = a;
@@ -375,98 +420,132 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
     }
     st.unit = 1.f;
     const float cdot = kLog2e / sqrtf((float)D);
-    WarpTile &tl = sm.tile[warp];
+    Tile &tl = sm.tile;
     const RecLoc L = rec_loc(c, s, h, 0);
-    const int a0 = min(e_all, (split * kWarps + warp) * share), a1 = min(e_all, a0 + share);
-    int a = a0;
-    while (a < a1) {
-        // a tile: up to kTileKeys entries of one kind
+    const int a0 = min(e_all, split * share), a1 = min(e_all, a0 + share);
+    for (int a = a0; a < a1;) {
+        // a tile: up to kTileKeys entries of one kind, the warps' parts multiples of 32
         const bool blocks = a < e_block;
         const int n = min(kTileKeys, (blocks ? min(a1, e_block) : a1) - a);
+        const int per = ((n + kWarps - 1) / kWarps + 31) & ~31;
+        const int p0 = warp * per, p1 = min(n, p0 + per);
         const uint32_t act = blocks ? full : local;
-        uint32_t mt[kTileKeys / 32];
-        float4 sd[kTileKeys / 32];
+        uint32_t mt[kSteps], bal[kSteps][4];
+        int64_t slot[kSteps];
         int cnt[4] = {0, 0, 0, 0};
-        float smax[4] = {0.f, 0.f, 0.f, 0.f};
+        if (tid < 4) sm.smax[tid] = 0u;
 #pragma unroll
-        for (int i = 0; i < kTileKeys / 32; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
             mt[i] = 0;
-            const int e = i * 32 + lane;
+            slot[i] = slot0;
+            const int e = a + p0 + i * 32 + lane;
+            if (p0 + i * 32 >= p1) continue;
             int j = -1;
-            if (e < n) {
+            if (e < a + p1) {
                 if (blocks) {
-                    const int x = (a + e) >> job.block_shift;
+                    const int x = e >> job.block_shift;
                     const int id = x < job.k ? job.ids[(int64_t)sh * job.k + x] : -1;
                     if (id >= 0) {
                         const int before = x > 0 ? job.ids[(int64_t)sh * job.k + x - 1] : -1;
                         if ((x > 0 && before < 0) || id <= before || id >= nb) {
                             set_status(c.status, KVQ_ERR_DEVICE_CHECK);
                         } else {
-                            j = (id << job.block_shift) + ((a + e) & ((1 << job.block_shift) - 1));
+                            j = (id << job.block_shift) + (e & ((1 << job.block_shift) - 1));
                             if (j >= len) j = -1;
                         }
                     }
                 } else {
-                    j = len - wl + (a - e_block) + e;
+                    j = len - wl + e - e_block;
                 }
             }
             if (j >= 0) {
-                mt[i] = c.meta[slot0 + j] | kValid;
-                sd[i] = c.side[slot0 + j];
+                slot[i] = slot0 + j;
+                mt[i] = c.meta[slot[i]] | kValid;
             }
         }
+        // 16 consecutive entries are consecutive keys, the valid ones in front: ask for their
+        // side entries and records
 #pragma unroll
-        for (int i = 0; i < kTileKeys / 32; ++i) {
+        for (int i = 0; i < kSteps; ++i) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) bal[i][w] = 0u;
+            if (p0 + i * 32 >= p1) continue;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const bool in = (mt[i] & 7u) == (kValid | w);
-                cnt[w] += __popc(__ballot_sync(0xffffffffu, in));
-                if (in) smax[w] = fmaxf(smax[w], sd[i].z);
+                bal[i][w] = __ballot_sync(0xffffffffu, (mt[i] & 7u) == (kValid | w));
+                cnt[w] += __popc(bal[i][w]);
+            }
+            const uint32_t ok = bal[i][0] | bal[i][1] | bal[i][2] | bal[i][3];
+            const int hb = lane & 16, keys = __popc((ok >> hb) & 0xFFFFu);
+            const uint32_t last = __shfl_sync(0xffffffffu, mt[i], hb + max(keys - 1, 0));
+            if (lane == hb && keys > 0) {
+                prefetch_l2(&c.side[slot[i]], 16u * keys);
+                prefetch_records<PAGED>(L, mt[i] & ~15u, (last & ~15u) + ((uint32_t)(D / 2) << (last & 3u)));
             }
         }
-        int first[5];
+        if (lane < 4) sm.cnt[warp][lane] = lane == 0 ? cnt[0] : lane == 1 ? cnt[1] : lane == 2 ? cnt[2] : cnt[3];
+        __syncthreads();
+        // slots: width by width, each width's keys in the warps' order, padded to 16
+        int all[4], at[4], first[5];
         first[0] = 0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) first[w + 1] = first[w] + ((cnt[w] + 15) & ~15);
-        int at[4] = {first[0], first[1], first[2], first[3]};
-        uint32_t some[4] = {0u, 0u, 0u, 0u};     // an offset of a real record of each width
+        for (int w = 0; w < 4; ++w) {
+            all[w] = 0;
+            at[w] = 0;
 #pragma unroll
-        for (int i = 0; i < kTileKeys / 32; ++i) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const bool in = (mt[i] & 7u) == (kValid | w);
-                const uint32_t b = __ballot_sync(0xffffffffu, in);
-                if (in) {
-                    const int pos = at[w] + __popc(b & ((1u << lane) - 1u));
-                    const float mid = w == 3 ? 0.f : (float)(1 << ((2 << w) - 1));
-                    tl.ent[pos] = mt[i];
-                    tl.side[pos] = make_float4(sd[i].x * cdot, fmaf(mid, sd[i].x, sd[i].y) * cdot, sd[i].z,
-                                               fmaf(mid, sd[i].z, sd[i].w));
-                    some[w] = mt[i];
-                }
-                at[w] += __popc(b);
+            for (int x = 0; x < kWarps; ++x) {
+                const int m = sm.cnt[x][w];
+                if (x < warp) at[w] += m;
+                all[w] += m;
             }
+            at[w] += first[w];
+            first[w + 1] = first[w] + ((all[w] + 15) & ~15);
         }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            if (p0 + i * 32 >= p1) continue;
+            const int w = mt[i] & 3;
+            const uint32_t b = w == 0 ? bal[i][0] : w == 1 ? bal[i][1] : w == 2 ? bal[i][2] : bal[i][3];
+            const int to = w == 0 ? at[0] : w == 1 ? at[1] : w == 2 ? at[2] : at[3];
+            float4 sd = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (mt[i] & kValid) {
+                sd = __ldg(&c.side[slot[i]]);
+                const int pos = to + __popc(b & ((1u << lane) - 1u));
+                const float mid = w == 3 ? 0.f : (float)(1 << ((2 << w) - 1));
+                tl.ent[pos] = mt[i];
+                tl.side[pos] = make_float4(sd.x * cdot, fmaf(mid, sd.x, sd.y) * cdot, sd.z, fmaf(mid, sd.z, sd.w));
+                sm.some[w] = mt[i];               // any one of them
+            }
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, w == x ? __float_as_uint(sd.z) : 0u);
+                if (lane == 0 && bal[i][x]) atomicMax(&sm.smax[x], top);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) at[x] += __popc(bal[i][x]);
+        }
+        __syncthreads();
         // padding up to 16: a real record's offset, no kValid
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            if (cnt[w] == 0) continue;
-            const uint32_t any = __reduce_max_sync(0xffffffffu, some[w]);
-            if (at[w] + lane < first[w + 1]) {
-                tl.ent[at[w] + lane] = any & ~kValid;
-                tl.side[at[w] + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int to = first[w] + all[w] + lane;
+            if (warp == w && all[w] > 0 && to < first[w + 1]) {
+                tl.ent[to] = sm.some[w] & ~kValid;
+                tl.side[to] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
-        __syncwarp();
+        __syncthreads();
         const bool on0 = (act >> (2 * t)) & 1u, on1 = (act >> (2 * t + 1)) & 1u;
+        const int chunks = first[4] / 16;
+        const int c0 = chunks * warp / kWarps * 16, c1 = chunks * (warp + 1) / kWarps * 16;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            if (cnt[w] == 0) continue;
+            const int b0 = max(c0, first[w]), b1 = min(c1, first[w + 1]);
+            if (b0 >= b1) continue;
             // weights in units of S / 64, S a power of two above the largest scale (1 for fp16 values)
             float fac = 64.f, unit = 0.015625f;
             if (w != 3) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(smax[w]));
-                const int e = min(max((int)(top >> 23) + 1, 87), 167);     // biased exponent of S
+                const int e = min(max((int)(sm.smax[w] >> 23) + 1, 87), 167);     // biased exponent of S
                 unit = __uint_as_float((uint32_t)(e - 6) << 23);
                 fac = __uint_as_float((uint32_t)(254 - e + 6) << 23);
             }
@@ -481,14 +560,13 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
                 }
                 st.unit = unit;
             }
-            const int len16 = first[w + 1] - first[w];
-            if (w == 0) run_class<D, 0>(st, sm, tl, L, first[w], len16, fac, on0, on1);
-            else if (w == 1) run_class<D, 1>(st, sm, tl, L, first[w], len16, fac, on0, on1);
-            else if (w == 2) run_class<D, 2>(st, sm, tl, L, first[w], len16, fac, on0, on1);
-            else run_class<D, 3>(st, sm, tl, L, first[w], len16, fac, on0, on1);
+            if (w == 0) run_class<D, 0, PAGED>(st, sm, L, b0, b1 - b0, fac, on0, on1);
+            else if (w == 1) run_class<D, 1, PAGED>(st, sm, L, b0, b1 - b0, fac, on0, on1);
+            else if (w == 2) run_class<D, 2, PAGED>(st, sm, L, b0, b1 - b0, fac, on0, on1);
+            else run_class<D, 3, PAGED>(st, sm, L, b0, b1 - b0, fac, on0, on1);
         }
-        __syncwarp();                            // the tile's slots are read; the next one overwrites them
         a += n;
+        __syncthreads();                         // the tile's slots are read; the next one overwrites them
     }
 
     // this warp's sums over its lanes, then the warps' states through shared memory
@@ -500,7 +578,6 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
             st.pz[i] += __shfl_xor_sync(0xffffffffu, st.pz[i], d);
         }
     }
-    __syncthreads();
     {
         const int g = lane >> 2;
 #pragma unroll
@@ -518,6 +595,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         }
     }
     __syncthreads();
+    const bool cluster = job.n_split > 1 && job.n_split <= kMaxCluster;
     for (int x = tid; x < nq * D; x += kThreads) {
         const int qi = x / D, ch = x % D;
         float M = kMInit, l = 0.f, o = 0.f;
@@ -531,15 +609,38 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         }
         if (job.n_split == 1) {
             out[(q0 + qi) * D + ch] = l > 0.f ? o / l : 0.f;
-        } else {
-            float *p = job.part + (((int64_t)unit * job.n_split + split) * job.qs + qi) * (D + 4);
-            p[ch] = o;
-            if (ch == 0) {
-                p[D] = M;
-                p[D + 1] = l;
-            }
+            continue;
+        }
+        float *p = cluster ? sm.done[qi] : job.part + (((int64_t)unit * job.n_split + split) * job.qs + qi) * (D + 4);
+        p[ch] = o;
+        if (ch == 0) {
+            p[D] = M;
+            p[D + 1] = l;
         }
     }
+    if (!cluster) return;
+    // the cluster's CTAs share the outputs; each reads every CTA's state
+    namespace cg = cooperative_groups;
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    for (int x = split * kThreads + tid; x < nq * D; x += job.n_split * kThreads) {
+        const int qi = x / D, ch = x % D;
+        float M = kMInit, l = 0.f, o = 0.f, m[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            m[r] = r < job.n_split ? cl.map_shared_rank(&sm.done[qi][D], r)[0] : kMInit;
+            M = fmaxf(M, m[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            if (r >= job.n_split) break;
+            const float f = ex2(m[r] - M);
+            l = fmaf(cl.map_shared_rank(&sm.done[qi][D + 1], r)[0], f, l);
+            o = fmaf(cl.map_shared_rank(&sm.done[qi][ch], r)[0], f, o);
+        }
+        out[(q0 + qi) * D + ch] = l > 0.f ? o / l : 0.f;
+    }
+    cl.sync();                                   // every CTA's state has been read
 }
 
 // Merges the n_split partial states of each (sequence, query head), a warp per output.
@@ -587,19 +688,36 @@ int splits(const kvq_cache *cache, int k, int block, int w)
     const int64_t keys_b = std::min<int64_t>((int64_t)k * block, ((int64_t)cache->max_cap + block - 1) / block * block);
     const int64_t keys_w = std::min<int64_t>((int64_t)w + 1, cache->max_cap);
     const int64_t keys = c.G == 1 ? std::max(keys_b, keys_w) : keys_b + keys_w;
-    const int64_t want = (12 * (int64_t)num_sms() + units * kWarps - 1) / (units * kWarps);
+    const int64_t want = ((int64_t)num_sms() + units - 1) / units;
     return (int)std::max<int64_t>(1, std::min<int64_t>(want, (keys + 64 * kWarps - 1) / (64 * kWarps)));
 }
 
-template <int D>
+template <int D, bool PAGED>
 cudaError_t launch_typed(const kvq_cache *cache, const __half *q, const Job &job, float *out, cudaStream_t st)
 {
     const CacheView &c = cache->view;
     const size_t smem = sizeof(Smem<D>);
-    cudaError_t e = ensure_smem_attr((const void *)decode_blocks_kernel<D>, smem);
+    cudaError_t e = ensure_smem_attr((const void *)decode_blocks_kernel<D, PAGED>, smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)c.B * c.H * job.n_sub;
-    e = launch_pdl(decode_blocks_kernel<D>, dim3((unsigned)(units * job.n_split)), dim3(kThreads), smem, st, c, q, job, out);
+    const dim3 grid((unsigned)(units * job.n_split));
+    if (job.n_split > 1 && job.n_split <= kMaxCluster) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)job.n_split;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, decode_blocks_kernel<D, PAGED>, c, q, job, out);
+    }
+    e = launch_pdl(decode_blocks_kernel<D, PAGED>, grid, dim3(kThreads), smem, st, c, q, job, out);
     if (e != cudaSuccess || job.n_split == 1) return e;
     const int64_t n_out = (int64_t)c.B * c.H * c.G;
     return launch_pdl(decode_blocks_combine_kernel<D>, dim3((unsigned)((n_out + kWarps - 1) / kWarps)), dim3(kThreads), 0, st,
@@ -612,7 +730,7 @@ int64_t decode_blocks_scratch(const kvq_cache *cache, int k, int block, int w)
 {
     const CacheView &c = cache->view;
     const int n = splits(cache, k, block, w);
-    if (n == 1) return 0;
+    if (n <= kMaxCluster) return 0;
     return (int64_t)c.B * c.H * ((c.G + kQ - 1) / kQ) * n * std::min(c.G, kQ) * (c.D + 4) * (int64_t)sizeof(float);
 }
 
@@ -630,7 +748,9 @@ cudaError_t launch_decode_blocks(const __half *q, const kvq_cache *cache, const 
     job.n_sub = (c.G + kQ - 1) / kQ;
     job.qs = std::min(c.G, kQ);
     job.part = scratch;
-    return c.D == 128 ? launch_typed<128>(cache, q, job, out, st) : launch_typed<64>(cache, q, job, out, st);
+    if (c.ptab)
+        return c.D == 128 ? launch_typed<128, true>(cache, q, job, out, st) : launch_typed<64, true>(cache, q, job, out, st);
+    return c.D == 128 ? launch_typed<128, false>(cache, q, job, out, st) : launch_typed<64, false>(cache, q, job, out, st);
 }
 
 } // namespace kvq

@@ -91,13 +91,12 @@ def _raise(code: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream, device):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+    # the handle alone: building a torch.cuda.Stream takes as long as a short kernel
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _on(device):
@@ -106,6 +105,9 @@ def _on(device):
 
 
 def _check(t, name, dtype, device, shape=None):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous() and \
+            (shape is None or t.shape == shape):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda" or t.device.index != device.index:
@@ -414,14 +416,12 @@ def routed_attn_decode_blocks(q, cache: KVQCache, ids, block: int, modes, w: int
     k, lib = ids.shape[2], load_library()
     need = lib.routed_attn_decode_blocks_scratch(cache.handle, k, block, int(w))
     with _on(dev):
-        st = torch.cuda.current_stream(dev) if stream is None else stream
         scratch = None
-        if need > 0:
-            # owned by this call: allocated for the stream that runs it
-            with torch.cuda.stream(st):
+        if need > 0:                 # this call's own: allocated for the stream that runs it
+            with torch.cuda.stream(stream):
                 scratch = torch.empty(need, dtype=torch.uint8, device=dev)
         _raise(lib.routed_attn_decode_blocks(_ptr(q), cache.handle, _ptr(ids), k, block, _ptr(modes), int(w),
-                                             _ptr(scratch), max(need, 0), _ptr(out), _stream(st, dev)))
+                                             _ptr(scratch), max(need, 0), _ptr(out), _stream(stream, dev)))
     return out
 
 
