@@ -5,28 +5,31 @@
 //
 //   logit_j = q . deq(k_j) / sqrt(D),  p = softmax,  out = sum_j p_j deq(v_j)
 //
-// With codes c, scale s, zero z (Eq. 4) and the centred codes c' = c - 2^(b-1) (b < 16; a small
-// integer, exact in fp16), z' = z + 2^(b-1) s:
-//   q . deq(k_j) = s_j (q . c'_j) + z'_j sum(q),   sum_j p_j deq(v_j) = sum_j (p_j s_j) c'_j + sum_j p_j z'_j
-// Centring keeps the two terms from cancelling: for normal rows |q . c'| is a tenth of |q . c|.
+// With codes c, scale s, zero z (Eq. 4), the centred codes c' = c - 2^(b-1) (b < 16) and
+// z' = z + 2^(b-1) s:
+//   q . deq(k_j) = s_j (q . c_j) + z_j sum(q),   sum_j p_j deq(v_j) = sum_j (p_j s_j) c'_j + sum_j p_j z'_j
+// Centring keeps the two sums of V, which run over many keys, from cancelling.
 //
 // One warp serves up to 8 query heads of a KV head at once with m16n8k16 matrix
 // instructions (fp16 operands, fp32 sums), 16 keys at a time:
-//   S^T [16 keys x 8 queries]      = C' [16 x D] . Q^T [D x 8]            D/16 instructions
-//   O^T [D channels x 8 queries]  += C'^T [D x 16] . W^T [16 x 8]         2 D/16 instructions
+//   S^T [16 keys x 8 queries]      = C [16 x D] . Q^T [D x 8]            D/16 instructions
+//   O^T [D channels x 8 queries]  += C'^T [D x 16] . W^T [16 x 8]        2 D/16 (up to 4 queries: D/16)
 // The products are exact: q, the codes and native values are fp16 numbers. The weights
 // w = p s are not, so each goes in as two fp16 numbers, w = hi + lo (22 bits), in units that
 // keep them far from fp16's subnormals: a power of two above the largest s_V among the
-// tile's keys of one width, times 2^-6 (p is at most 2^8, see below). The queries are too few
-// for the 128-row tiles of tcgen05 (G is 1 to 64, and the codes would have to be unpacked to
-// shared memory first); the loads, not the products, are what the time goes to.
+// tile's keys of one width, times 2^-6 (p is at most 2^8, see below). Up to 4 queries leave
+// columns 4..7 of the instruction to the second numbers. The queries are too few for the
+// 128-row tiles of tcgen05 (G is 1 to 64, and the codes would have to be unpacked to shared
+// memory first).
 //
 // The keys of a tile (up to 1024 of a CTA's share) are first sorted by width, so that 16 keys
-// of one width unpack by one code path, and the warps take equal runs of 16-key steps. A
-// 16-bit half of a word holds 16/b codes; one mask-and-or puts field i of both halves into the
-// mantissa of the power of two 2^(10 - b i) whose last place there is 1, the pair 2^(10 - b i) + c,
-// and one addition takes it to c'. For K the two halves are channels of one key (q is stored in the matching order, one
-// order per width); for V they are the same channels of two keys (one byte permutation).
+// of one width unpack by one code path; the warps take the 16-key steps in turn. A 16-bit
+// half of a word holds 16/b codes. For K the two halves are channels of one key (q is stored
+// in the matching order, one order per width) and a mask alone makes an operand: a field in
+// place IS the fp16 subnormal c 2^(pos - 24), and the sums of each position are scaled once
+// per key. For V the halves are the same channels of two keys (one byte permutation), and
+// the fields join the mantissa of 2^(10 - pos), whose last place there is 1, before
+// 2^(10 - pos) + 2^(b-1) is subtracted.
 //
 // Online softmax: the running maximum of a query moves only when a logit exceeds it by
 // more than 8 (log2 units), a warp-uniform branch. The warps of a CTA share a (sequence, KV
@@ -57,7 +60,7 @@ constexpr int kMaxCluster = 8;                   // CTAs of a cluster
 constexpr uint32_t kValid = 4u;                  // meta bit of a real key (bits 0..1: width code)
 
 struct Tile {
-    float4 side[kSlots];                         // (s_K cdot, z'_K cdot, s_V, z'_V), sorted
+    float4 side[kSlots];                         // (s_K cdot 2^24 (fp16: cdot), z_K cdot, s_V, z'_V), sorted
     uint32_t ent[kSlots];                        // record offset | kValid | width code, sorted
 };
 
@@ -97,51 +100,75 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)     // an 8x8 matrix 
     return y;
 }
 
+// (a, b) minus the fp16 pair h, as an fp16 pair
+__device__ __forceinline__ uint32_t rest_half(float a, float b, uint32_t h)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    const __half2 r = __floats2half2_rn(a - f.x, b - f.y);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi)
 {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// (field of SHIFT's bits in both halves of p) - 2^(BITS - 1): the field joins the mantissa of
-// 2^(10 - SHIFT), then 2^(10 - SHIFT) + 2^(BITS - 1) is subtracted; every step is exact.
+// The field of BITS bits at SHIFT in both halves of p as fp16 subnormals: c 2^(SHIFT - 24) each.
 template <int BITS, int SHIFT>
-__device__ __forceinline__ uint32_t field(uint32_t p)
+__device__ __forceinline__ uint32_t raw_field(uint32_t p)
 {
-    constexpr uint32_t mask = (((1u << BITS) - 1u) << SHIFT) * 0x10001u;
+    return p & ((((1u << BITS) - 1u) << SHIFT) * 0x10001u);
+}
+
+// The same field centred, c - 2^(BITS - 1): it joins the mantissa of 2^(10 - SHIFT), whose last
+// place there is 1, then 2^(10 - SHIFT) + 2^(BITS - 1) is subtracted; every step is exact.
+template <int BITS, int SHIFT>
+__device__ __forceinline__ uint32_t mid_field(uint32_t p)
+{
     constexpr uint32_t magic = (uint32_t)((25 - SHIFT) << 10) * 0x10001u;
     constexpr uint32_t off = (0x8000u | (uint32_t)((25 - SHIFT) << 10) | (1u << (BITS - 1 + SHIFT))) * 0x10001u;
-    const uint32_t x = (p & mask) | magic, m = off;
+    const uint32_t x = raw_field<BITS, SHIFT>(p) | magic, m = off;
     const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&m));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // The 16/BITS centred codes in each half of p (LSB-first) as fp16 pairs: x[i] = (field i of
-// the low half, field i of the high half) - 2^(BITS-1); p itself for 16-bit values.
+// the low half, field i of the high half) - 2^(BITS-1).
 template <int BITS>
-__device__ __forceinline__ void fields(uint32_t p, uint32_t (&x)[16 / BITS])
+__device__ __forceinline__ void mid_fields(uint32_t p, uint32_t (&x)[16 / BITS])
 {
-    if constexpr (BITS == 16) {
-        x[0] = p;
-    } else if constexpr (BITS == 8) {
-        x[0] = field<8, 0>(p);
-        x[1] = field<8, 0>(p >> 8);
+    const uint32_t h = p >> 8;
+    if constexpr (BITS == 8) {
+        x[0] = mid_field<8, 0>(p);
+        x[1] = mid_field<8, 0>(h);
     } else if constexpr (BITS == 4) {
-        const uint32_t h = p >> 8;
-        x[0] = field<4, 0>(p);
-        x[1] = field<4, 4>(p);
-        x[2] = field<4, 0>(h);
-        x[3] = field<4, 4>(h);
+        x[0] = mid_field<4, 0>(p);
+        x[1] = mid_field<4, 4>(p);
+        x[2] = mid_field<4, 0>(h);
+        x[3] = mid_field<4, 4>(h);
     } else {
-        const uint32_t h = p >> 8;
-        x[0] = field<2, 0>(p);
-        x[1] = field<2, 2>(p);
-        x[2] = field<2, 4>(p);
-        x[3] = field<2, 6>(p);
-        x[4] = field<2, 0>(h);
-        x[5] = field<2, 2>(h);
-        x[6] = field<2, 4>(h);
-        x[7] = field<2, 6>(h);
+        x[0] = mid_field<2, 0>(p);
+        x[1] = mid_field<2, 2>(p);
+        x[2] = mid_field<2, 4>(p);
+        x[3] = mid_field<2, 6>(p);
+        x[4] = mid_field<2, 0>(h);
+        x[5] = mid_field<2, 2>(h);
+        x[6] = mid_field<2, 4>(h);
+        x[7] = mid_field<2, 6>(h);
+    }
+}
+
+// One word of K of two keys (rows g: x, g + 8: y) against its query operands: s[SHIFT / BITS]
+// gains q . c 2^(SHIFT - 24) over the word's fields at SHIFT and SHIFT + 8 of both halves.
+template <int BITS, int SHIFT>
+__device__ __forceinline__ void k_fields(float (&s)[4][4], uint32_t x, uint32_t y, const uint32_t *q)
+{
+    if constexpr (SHIFT < 8) {
+        constexpr int f = SHIFT / BITS;
+        mma(s[f], raw_field<BITS, SHIFT>(x), raw_field<BITS, SHIFT>(y), raw_field<BITS, SHIFT>(x >> 8),
+            raw_field<BITS, SHIFT>(y >> 8), q[f], q[f + 8 / BITS]);
+        k_fields<BITS, SHIFT + BITS>(s, x, y, q);
     }
 }
 
@@ -161,14 +188,14 @@ __device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes)
 template <bool PAGED>
 __device__ __forceinline__ void prefetch_records(const RecLoc &L, uint32_t o0, uint32_t o1)
 {
-    if (!PAGED) {
+    if constexpr (!PAGED) {
         prefetch_l2(L.base + o0, o1 - o0);
-        return;
-    }
-    while (o0 < o1) {
-        const uint32_t n = min(o1 - o0, (1u << L.shift) - (o0 & ((1u << L.shift) - 1u)));
-        prefetch_l2(L.at(o0), n);
-        o0 += n;
+    } else {
+        while (o0 < o1) {
+            const uint32_t n = min(o1 - o0, (1u << L.shift) - (o0 & ((1u << L.shift) - 1u)));
+            prefetch_l2(L.at(o0), n);
+            o0 += n;
+        }
     }
 }
 
@@ -207,9 +234,10 @@ struct State {
     float unit;
 };
 
-// Slots base .. base + n - 1 of the sorted tile, all of width 2 << CLS, 16 at a time.
-template <int D, int CLS, bool PAGED>
-__device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const RecLoc &L, int base, int n, float fac, bool on0,
+// Slots base, base + 16 kWarps, .. below `end` of the sorted tile, 16 at a time, all of width
+// 2 << CLS.
+template <int D, int CLS, bool PAGED, int NQ>
+__device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const RecLoc &L, int base, int end, float fac, bool on0,
                                           bool on1)
 {
     const Tile &tl = sm.tile;
@@ -228,7 +256,7 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
         q[4 * i + 3] = x.w;
     }
     const float qs0 = sm.qsum[2 * t], qs1 = sm.qsum[2 * t + 1];
-    for (int c = base; c < base + n; c += 16) {
+    for (int c = base; c < end; c += 16 * kWarps) {
         const uint32_t e0 = tl.ent[c + g], e1 = tl.ent[c + 8 + g];
         const uint2 f0 = *reinterpret_cast<const uint2 *>(&tl.ent[c + 2 * t]);
         const uint2 f1 = *reinterpret_cast<const uint2 *>(&tl.ent[c + 8 + 2 * t]);
@@ -241,22 +269,29 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
         load_bytes<VB, PAGED>(L, (f0.y & ~15u) + vo, v[1]);
         load_bytes<VB, PAGED>(L, (f1.x & ~15u) + vo, v[2]);
         load_bytes<VB, PAGED>(L, (f1.y & ~15u) + vo, v[3]);
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-        // a word gives F operand pairs of its key; two of them make one instruction's depth of 16
+        // S^T: a word gives 16/BITS operand pairs of its key; equal fields share a sum (for wide codes
+        // two sums alternate), so no chain of dependent instructions is longer than 4
+        float sf[4][4];
 #pragma unroll
-        for (int i = 0; i < KW; i += (F == 1 ? 2 : 1)) {
-            uint32_t a[F == 1 ? 2 : F], b[F == 1 ? 2 : F];
-            if constexpr (F == 1) {
-                a[0] = k0[i];
-                a[1] = k0[i + 1];
-                b[0] = k1[i];
-                b[1] = k1[i + 1];
-            } else {
-                fields<BITS>(k0[i], a);
-                fields<BITS>(k1[i], b);
-            }
+        for (int i = 0; i < 4; ++i) sf[i][0] = sf[i][1] = sf[i][2] = sf[i][3] = 0.f;
+        if constexpr (CLS == 3) {
 #pragma unroll
-            for (int f = 0; f < (F == 1 ? 2 : F); f += 2) mma(s, a[f], b[f], a[f + 1], b[f + 1], q[i * F + f], q[i * F + f + 1]);
+            for (int i = 0; i < KW; i += 2) mma(sf[i / 2 & 1], k0[i], k1[i], k0[i + 1], k1[i + 1], q[i], q[i + 1]);
+        } else if constexpr (CLS == 2) {
+#pragma unroll
+            for (int i = 0; i < KW; ++i)
+                mma(sf[i & 1], raw_field<8, 0>(k0[i]), raw_field<8, 0>(k1[i]), raw_field<8, 0>(k0[i] >> 8),
+                    raw_field<8, 0>(k1[i] >> 8), q[2 * i], q[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < KW; ++i) k_fields<BITS, 0>(sf, k0[i], k1[i], q + i * F);
+        }
+        float s[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (CLS >= 2) s[i] = sf[0][i] + sf[1][i];
+            else if (CLS == 1) s[i] = fmaf(sf[1][i], 0.0625f, sf[0][i]);
+            else s[i] = fmaf(fmaf(fmaf(sf[3][i], 0.25f, sf[2][i]), 0.25f, sf[1][i]), 0.25f, sf[0][i]);
         }
         const float4 sd0 = tl.side[c + g], sd1 = tl.side[c + 8 + g];
         const bool v0 = e0 & kValid, v1 = e1 & kValid;
@@ -288,7 +323,7 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
                 st.o[i][3] *= c1;
             }
         }
-        float p[4], hi[4], lo[4];
+        float p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[i] = ex2(lg[i] - st.m[i & 1]);
         st.l[0] += p[0] + p[2];
@@ -298,14 +333,22 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
             st.pz[1] = fmaf(p[1], sd0.w, fmaf(p[3], sd1.w, st.pz[1]));
         }
         const float w0 = CLS == 3 ? fac : sd0.z * fac, w1 = CLS == 3 ? fac : sd1.z * fac;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float w = p[i] * (i < 2 ? w0 : w1);
-            hi[i] = __half2float(__float2half_rn(w));
-            lo[i] = w - hi[i];
+        p[0] *= w0;
+        p[1] *= w0;
+        p[2] *= w1;
+        p[3] *= w1;
+        uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
+        const uint32_t r0 = rest_half(p[0], p[1], h0), r1 = rest_half(p[2], p[3], h1);
+        uint32_t bh0, bh1, bl0 = 0u, bl1 = 0u;
+        if (NQ == 4) {                           // columns 4..7 carry the rests of queries 0..3
+            bh0 = transpose8(t < 2 ? h0 : r0);
+            bh1 = transpose8(t < 2 ? h1 : r1);
+        } else {
+            bh0 = transpose8(h0);
+            bh1 = transpose8(h1);
+            bl0 = transpose8(r0);
+            bl1 = transpose8(r1);
         }
-        const uint32_t bh0 = transpose8(pack_half(hi[0], hi[1])), bh1 = transpose8(pack_half(hi[2], hi[3]));
-        const uint32_t bl0 = transpose8(pack_half(lo[0], lo[1])), bl1 = transpose8(pack_half(lo[2], lo[3]));
         // word i of the four keys, half by half: channels (32 i + 16 half)/BITS + field
 #pragma unroll
         for (int i = 0; i < (VB + 3) / 4; ++i) {
@@ -318,17 +361,17 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
                     if (half == 0) {
                         const uint32_t qa = __byte_perm(v[0][i], v[1][i], 0x7632), qb = __byte_perm(v[2][i], v[3][i], 0x7632);
                         mma(st.o[i], pa, qa, pb, qb, bh0, bh1);
-                        mma(st.o[i], pa, qa, pb, qb, bl0, bl1);
+                        if (NQ == 8) mma(st.o[i], pa, qa, pb, qb, bl0, bl1);
                     }
                 } else {
                     uint32_t xa[F], xb[F];
-                    fields<BITS>(pa, xa);
-                    fields<BITS>(pb, xb);
+                    mid_fields<BITS>(pa, xa);
+                    mid_fields<BITS>(pb, xb);
 #pragma unroll
                     for (int f = 0; f < F; f += 2) {
                         const int mt = ((2 * i + half) * F + f) / 2;
                         mma(st.o[mt], xa[f], xa[f + 1], xb[f], xb[f + 1], bh0, bh1);
-                        mma(st.o[mt], xa[f], xa[f + 1], xb[f], xb[f + 1], bl0, bl1);
+                        if (NQ == 8) mma(st.o[mt], xa[f], xa[f + 1], xb[f], xb[f + 1], bl0, bl1);
                     }
                 }
             }
@@ -343,7 +386,7 @@ struct Job {
     float *part;                                 // [unit][n_split][qs][D + 4]
 };
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, int NQ>
 __global__ void __launch_bounds__(kThreads, 2)
 decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *__restrict__ out)
 {
@@ -353,7 +396,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
     pdl_trigger();
     const int split = blockIdx.x % job.n_split, unit = blockIdx.x / job.n_split;
     const int sub = unit % job.n_sub, sh = unit / job.n_sub, s = sh / c.H, h = sh % c.H;
-    const int g0 = sub * kQ, nq = min(kQ, c.G - g0);
+    const int g0 = sub * NQ, nq = min(NQ, c.G - g0);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, t = lane & 3;
     const int64_t q0 = (int64_t)sh * c.G + g0;   // first query head of the unit
     const int len = c.len[sh];
@@ -392,7 +435,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int p = 4 * i + e;             // operand pair: word p / f, field p % f
-            const __half *src = &sm.rows[ln >> 2][ch0 + ((p >> fl) << (fl + 1)) + (p & (f - 1))];
+            const __half *src = &sm.rows[(ln >> 2) & (NQ - 1)][ch0 + ((p >> fl) << (fl + 1)) + (p & (f - 1))];
             const __half2 v = __halves2half2(src[0], src[f]);
             r[e] = *reinterpret_cast<const uint32_t *>(&v);
         }
@@ -403,7 +446,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         const int qi = warp;
         float a = 0.f;
 #pragma unroll
-        for (int ch = 0; ch < D; ch += 32) a += __half2float(sm.rows[qi][ch + lane]);
+        for (int ch = 0; ch < D; ch += 32) a += __half2float(sm.rows[qi & (NQ - 1)][ch + lane]);
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) a += __shfl_xor_sync(0xffffffffu, a, d);
         if (lane == 0) sm.qsum[qi] = a;
@@ -513,7 +556,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
                 const int pos = to + __popc(b & ((1u << lane) - 1u));
                 const float mid = w == 3 ? 0.f : (float)(1 << ((2 << w) - 1));
                 tl.ent[pos] = mt[i];
-                tl.side[pos] = make_float4(sd.x * cdot, fmaf(mid, sd.x, sd.y) * cdot, sd.z, fmaf(mid, sd.z, sd.w));
+                tl.side[pos] = make_float4(sd.x * (w == 3 ? cdot : cdot * 16777216.f), sd.y * cdot, sd.z, fmaf(mid, sd.z, sd.w));
                 sm.some[w] = mt[i];               // any one of them
             }
 #pragma unroll
@@ -535,12 +578,11 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
             }
         }
         __syncthreads();
-        const bool on0 = (act >> (2 * t)) & 1u, on1 = (act >> (2 * t + 1)) & 1u;
-        const int chunks = first[4] / 16;
-        const int c0 = chunks * warp / kWarps * 16, c1 = chunks * (warp + 1) / kWarps * 16;
+        const bool on0 = (act >> (2 * t & (NQ - 1))) & 1u, on1 = (act >> ((2 * t & (NQ - 1)) + 1)) & 1u;
+        // 16-key steps dealt to the warps in turn, so that they run one width's code at a time
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const int b0 = max(c0, first[w]), b1 = min(c1, first[w + 1]);
+            const int b0 = first[w] + ((warp - first[w] / 16) & (kWarps - 1)) * 16, b1 = first[w + 1];
             if (b0 >= b1) continue;
             // weights in units of S / 64, S a power of two above the largest scale (1 for fp16 values)
             float fac = 64.f, unit = 0.015625f;
@@ -560,10 +602,10 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
                 }
                 st.unit = unit;
             }
-            if (w == 0) run_class<D, 0, PAGED>(st, sm, L, b0, b1 - b0, fac, on0, on1);
-            else if (w == 1) run_class<D, 1, PAGED>(st, sm, L, b0, b1 - b0, fac, on0, on1);
-            else if (w == 2) run_class<D, 2, PAGED>(st, sm, L, b0, b1 - b0, fac, on0, on1);
-            else run_class<D, 3, PAGED>(st, sm, L, b0, b1 - b0, fac, on0, on1);
+            if (w == 0) run_class<D, 0, PAGED, NQ>(st, sm, L, b0, b1, fac, on0, on1);
+            else if (w == 1) run_class<D, 1, PAGED, NQ>(st, sm, L, b0, b1, fac, on0, on1);
+            else if (w == 2) run_class<D, 2, PAGED, NQ>(st, sm, L, b0, b1, fac, on0, on1);
+            else run_class<D, 3, PAGED, NQ>(st, sm, L, b0, b1, fac, on0, on1);
         }
         a += n;
         __syncthreads();                         // the tile's slots are read; the next one overwrites them
@@ -578,7 +620,13 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
             st.pz[i] += __shfl_xor_sync(0xffffffffu, st.pz[i], d);
         }
     }
-    {
+    if (NQ == 4) {                               // the rests join their queries
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st.o[mt][i] += __shfl_down_sync(0xffffffffu, st.o[mt][i], 2);
+    }
+    if (2 * t < nq) {
         const int g = lane >> 2;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -646,7 +694,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
 // Merges the n_split partial states of each (sequence, query head), a warp per output.
 template <int D>
 __global__ void __launch_bounds__(kThreads)
-decode_blocks_combine_kernel(Job job, int64_t n_out, int G, float *__restrict__ out)
+decode_blocks_combine_kernel(Job job, int64_t n_out, int G, int nq, float *__restrict__ out)
 {
     constexpr int N = D / 32;
     pdl_wait();
@@ -654,8 +702,8 @@ decode_blocks_combine_kernel(Job job, int64_t n_out, int G, float *__restrict__ 
     const int64_t hq = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (hq >= n_out) return;
     const int lane = threadIdx.x & 31, g = (int)(hq % G);
-    const int64_t unit = hq / G * job.n_sub + g / kQ;
-    const float *p = job.part + (unit * job.n_split * job.qs + g % kQ) * (D + 4);
+    const int64_t unit = hq / G * job.n_sub + g / nq;
+    const float *p = job.part + (unit * job.n_split * job.qs + g % nq) * (D + 4);
     const int64_t step = (int64_t)job.qs * (D + 4);
     float M = kMInit;
     for (int i = lane; i < job.n_split; i += 32) M = fmaxf(M, p[i * step + D]);
@@ -679,12 +727,17 @@ int shift_of(int block)
     return s;
 }
 
+// Query heads a warp serves: groups of up to 4 leave room for the weights' second halves in
+// the same instructions.
+int queries_per_warp(int G) { return G <= 4 ? 4 : kQ; }
+int subgroups(int G) { return (G + queries_per_warp(G) - 1) / queries_per_warp(G); }
+
 // CTAs per (sequence, KV head, subgroup): enough for a few warps on every SM, at least 64 keys
 // a warp.
 int splits(const kvq_cache *cache, int k, int block, int w)
 {
     const CacheView &c = cache->view;
-    const int64_t units = (int64_t)c.B * c.H * ((c.G + kQ - 1) / kQ);
+    const int64_t units = (int64_t)c.B * c.H * (subgroups(c.G));
     const int64_t keys_b = std::min<int64_t>((int64_t)k * block, ((int64_t)cache->max_cap + block - 1) / block * block);
     const int64_t keys_w = std::min<int64_t>((int64_t)w + 1, cache->max_cap);
     const int64_t keys = c.G == 1 ? std::max(keys_b, keys_w) : keys_b + keys_w;
@@ -692,12 +745,12 @@ int splits(const kvq_cache *cache, int k, int block, int w)
     return (int)std::max<int64_t>(1, std::min<int64_t>(want, (keys + 64 * kWarps - 1) / (64 * kWarps)));
 }
 
-template <int D, bool PAGED>
+template <int D, bool PAGED, int NQ>
 cudaError_t launch_typed(const kvq_cache *cache, const __half *q, const Job &job, float *out, cudaStream_t st)
 {
     const CacheView &c = cache->view;
     const size_t smem = sizeof(Smem<D>);
-    cudaError_t e = ensure_smem_attr((const void *)decode_blocks_kernel<D, PAGED>, smem);
+    cudaError_t e = ensure_smem_attr((const void *)decode_blocks_kernel<D, PAGED, NQ>, smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)c.B * c.H * job.n_sub;
     const dim3 grid((unsigned)(units * job.n_split));
@@ -715,13 +768,23 @@ cudaError_t launch_typed(const kvq_cache *cache, const __half *q, const Job &job
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, decode_blocks_kernel<D, PAGED>, c, q, job, out);
+        return cudaLaunchKernelEx(&cfg, decode_blocks_kernel<D, PAGED, NQ>, c, q, job, out);
     }
-    e = launch_pdl(decode_blocks_kernel<D, PAGED>, grid, dim3(kThreads), smem, st, c, q, job, out);
+    e = launch_pdl(decode_blocks_kernel<D, PAGED, NQ>, grid, dim3(kThreads), smem, st, c, q, job, out);
     if (e != cudaSuccess || job.n_split == 1) return e;
     const int64_t n_out = (int64_t)c.B * c.H * c.G;
     return launch_pdl(decode_blocks_combine_kernel<D>, dim3((unsigned)((n_out + kWarps - 1) / kWarps)), dim3(kThreads), 0, st,
-                      job, n_out, c.G, out);
+                      job, n_out, c.G, NQ, out);
+}
+
+template <int NQ>
+cudaError_t launch_nq(const kvq_cache *cache, const __half *q, const Job &job, float *out, cudaStream_t st)
+{
+    if (cache->view.ptab)
+        return cache->D == 128 ? launch_typed<128, true, NQ>(cache, q, job, out, st)
+                               : launch_typed<64, true, NQ>(cache, q, job, out, st);
+    return cache->D == 128 ? launch_typed<128, false, NQ>(cache, q, job, out, st)
+                           : launch_typed<64, false, NQ>(cache, q, job, out, st);
 }
 
 } // namespace
@@ -731,7 +794,7 @@ int64_t decode_blocks_scratch(const kvq_cache *cache, int k, int block, int w)
     const CacheView &c = cache->view;
     const int n = splits(cache, k, block, w);
     if (n <= kMaxCluster) return 0;
-    return (int64_t)c.B * c.H * ((c.G + kQ - 1) / kQ) * n * std::min(c.G, kQ) * (c.D + 4) * (int64_t)sizeof(float);
+    return (int64_t)c.B * c.H * (subgroups(c.G)) * n * std::min(c.G, queries_per_warp(c.G)) * (c.D + 4) * (int64_t)sizeof(float);
 }
 
 cudaError_t launch_decode_blocks(const __half *q, const kvq_cache *cache, const int32_t *ids, int k, int block,
@@ -745,12 +808,11 @@ cudaError_t launch_decode_blocks(const __half *q, const kvq_cache *cache, const 
     job.block_shift = shift_of(block);
     job.w = w;
     job.n_split = splits(cache, k, block, w);
-    job.n_sub = (c.G + kQ - 1) / kQ;
-    job.qs = std::min(c.G, kQ);
+    job.n_sub = subgroups(c.G);
+    job.qs = std::min(c.G, queries_per_warp(c.G));
     job.part = scratch;
-    if (c.ptab)
-        return c.D == 128 ? launch_typed<128, true>(cache, q, job, out, st) : launch_typed<64, true>(cache, q, job, out, st);
-    return c.D == 128 ? launch_typed<128, false>(cache, q, job, out, st) : launch_typed<64, false>(cache, q, job, out, st);
+    if (queries_per_warp(c.G) == 4) return launch_nq<4>(cache, q, job, out, st);
+    return launch_nq<8>(cache, q, job, out, st);
 }
 
 } // namespace kvq
