@@ -193,6 +193,18 @@ cudaError_t ensure_smem_attr(const void *func, size_t bytes)
     return err;
 }
 
+cudaError_t ensure_cluster_attr(const void *func)
+{
+    static std::vector<std::pair<const void *, int>> done;
+    const int dev = current_device();
+    std::lock_guard<std::mutex> lock(g_dev_mu);
+    for (const auto &e : done)
+        if (e.first == func && e.second == dev) return cudaSuccess;
+    const cudaError_t err = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (err == cudaSuccess) done.emplace_back(func, dev);
+    return err;
+}
+
 // Testing hook state: the n-th device allocation of the next cache creation fails.
 std::atomic<int> g_fail_alloc_nth{0};
 

@@ -16,8 +16,9 @@
 //   O^T [D channels x 8 queries]  += C'^T [D x 16] . W^T [16 x 8]        2 D/16 (up to 4 queries: D/16)
 // The products are exact: q, the codes and native values are fp16 numbers. The weights
 // w = p s are not, so each goes in as two fp16 numbers, w = hi + lo (22 bits), in units that
-// keep them far from fp16's subnormals: a power of two above the largest s_V among the
-// tile's keys of one width, times 2^-6 (p is at most 2^8, see below). Up to 4 queries leave
+// keep them far from fp16's subnormals: a power of two above the s_V of the keys at hand (1 for
+// native values), times 2^-11 (p is at most 2^3, see below), chosen anew where a width's keys
+// begin and raised where a larger s_V comes. Up to 4 queries leave
 // columns 4..7 of the instruction to the second numbers. The queries are too few for the
 // 128-row tiles of tcgen05 (G is 1 to 64, and the codes would have to be unpacked to shared
 // memory first).
@@ -32,8 +33,8 @@
 // 2^(10 - pos) + 2^(b-1) is subtracted.
 //
 // Online softmax: the running maximum of a query moves only when a logit exceeds it by
-// more than 8 (log2 units), a warp-uniform branch. The warps of a CTA share a (sequence, KV
-// head) and merge at the end; up to 8 CTAs that share one form a cluster and merge through
+// more than 3 (log2 units), a warp-uniform branch. The warps of a CTA share a (sequence, KV
+// head) and merge at the end; up to 16 CTAs that share one form a cluster and merge through
 // distributed shared memory; more of them leave partial states in the caller's scratch, which
 // a second launch merges.
 //
@@ -49,19 +50,18 @@
 namespace kvq {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kQ = 8;                            // query heads per warp
-constexpr int kSteps = 4;                        // 32-key steps of a warp's part of a tile
+constexpr int kSteps = 8;                        // 32-key steps of a warp's part of a tile
 constexpr int kTileKeys = kWarps * kSteps * 32;  // keys sorted by width at a time
 constexpr int kSlots = kTileKeys + 4 * 16;       // each width's keys are padded to 16
-constexpr float kLazy = 8.f;                     // running-max slack, log2 units
+constexpr float kLazy = 3.f;                     // running-max slack, log2 units
 constexpr float kMInit = -1e30f;                 // running max before the first key
-constexpr int kMaxCluster = 8;                   // CTAs of a cluster
+constexpr int kMaxCluster = 16;                  // CTAs of a cluster
 constexpr uint32_t kValid = 4u;                  // meta bit of a real key (bits 0..1: width code)
 
 struct Tile {
-    float4 side[kSlots];                         // (s_K cdot 2^24 (fp16: cdot), z_K cdot, s_V, z'_V), sorted
-    uint32_t ent[kSlots];                        // record offset | kValid | width code, sorted
+    uint2 ent[kSlots];                           // (record offset | kValid | width code, key), sorted
 };
 
 template <int D>
@@ -75,7 +75,8 @@ struct Smem {
     float qsum[kQ];
     float done[kQ][D + 4];                       // the CTA's state for the cluster: o, then m and l
     int cnt[kWarps][4];                          // keys of each width in each warp's part of the tile
-    uint32_t some[4], smax[4];                   // per width: a real key's entry; the largest s_V's bits
+    uint2 some[4];                               // per width: a real key's entry
+    int32_t ids[kTileKeys / 16 + 2];             // the tile's blocks, from the one before its first on
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -234,17 +235,57 @@ struct State {
     float unit;
 };
 
+// The state's unit becomes S / 2^11, S the power of two above the scale whose bits are `top`.
+template <int D>
+__device__ __forceinline__ void set_unit(State<D> &st, uint32_t top)
+{
+    const int e = min(max((int)(top >> 23) + 1, 87), 167);      // biased exponent of S
+    const float unit = __uint_as_float((uint32_t)(e - 11) << 23), r = st.unit / unit;   // exact
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        st.o[i][0] *= r;
+        st.o[i][1] *= r;
+        st.o[i][2] *= r;
+        st.o[i][3] *= r;
+    }
+    st.unit = unit;
+}
+
+// K's words and the side entries of a 16-key step's rows g and g + 8.
+template <int D, int CLS, bool PAGED>
+struct KRows {
+    static constexpr int KW = D * (2 << CLS) / 128;      // words of a lane's D/4 channels of K
+    uint32_t a[KW], b[KW];
+    float4 sa, sb;
+    bool va, vb;
+    __device__ __forceinline__ void load(const Tile &tl, const RecLoc &L, const float4 *side, int c, int g, int t)
+    {
+        const uint2 e0 = tl.ent[c + g], e1 = tl.ent[c + 8 + g];
+        load_bytes<KW * 4, PAGED>(L, (e0.x & ~15u) + 4 * KW * t, a);
+        load_bytes<KW * 4, PAGED>(L, (e1.x & ~15u) + 4 * KW * t, b);
+        if (CLS != 3) {
+            sa = __ldg(side + e0.y);
+            sb = __ldg(side + e1.y);
+        }
+        va = e0.x & kValid;
+        vb = e1.x & kValid;
+    }
+};
+
 // Slots base, base + 16 kWarps, .. below `end` of the sorted tile, 16 at a time, all of width
-// 2 << CLS.
+// 2 << CLS. The next step's K and side entries are loaded while this one's weights are formed
+// (not for native values, whose words take the registers), V while this one's logits are.
 template <int D, int CLS, bool PAGED, int NQ>
-__device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const RecLoc &L, int base, int end, float fac, bool on0,
-                                          bool on1)
+__device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const RecLoc &L, const float4 *side, int base, int end,
+                                          bool on0, bool on1)
 {
     const Tile &tl = sm.tile;
     constexpr int BITS = 2 << CLS;
-    constexpr int KW = D * BITS / 128;           // words of a lane's D/4 channels of K
+    constexpr int KW = KRows<D, CLS, PAGED>::KW;
     constexpr int VB = D * BITS / 64;            // bytes of a lane's D/8 channels of V
     constexpr int F = 16 / BITS;                 // fields per half word
+    constexpr float mid = (float)(1 << (BITS - 1));
+    const float cdot = kLog2e / sqrtf((float)D);
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint32_t q[D / 8];
 #pragma unroll
@@ -255,20 +296,23 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
         q[4 * i + 2] = x.z;
         q[4 * i + 3] = x.w;
     }
-    const float qs0 = sm.qsum[2 * t], qs1 = sm.qsum[2 * t + 1];
+    const float qs0 = sm.qsum[2 * t] * cdot, qs1 = sm.qsum[2 * t + 1] * cdot;
+    KRows<D, CLS, PAGED> kr;
+    kr.load(tl, L, side, base, g, t);
+    if (CLS == 3) set_unit(st, 0x3F800000u);
+    else set_unit(st, __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(kr.sa.z, kr.sb.z))));
     for (int c = base; c < end; c += 16 * kWarps) {
-        const uint32_t e0 = tl.ent[c + g], e1 = tl.ent[c + 8 + g];
-        const uint2 f0 = *reinterpret_cast<const uint2 *>(&tl.ent[c + 2 * t]);
-        const uint2 f1 = *reinterpret_cast<const uint2 *>(&tl.ent[c + 8 + 2 * t]);
-        uint32_t k0[KW], k1[KW];
-        load_bytes<KW * 4, PAGED>(L, (e0 & ~15u) + 4 * KW * t, k0);
-        load_bytes<KW * 4, PAGED>(L, (e1 & ~15u) + 4 * KW * t, k1);
         uint32_t v[4][(VB + 3) / 4];
-        const uint32_t vo = D * BITS / 8 + VB * g;
-        load_bytes<VB, PAGED>(L, (f0.x & ~15u) + vo, v[0]);
-        load_bytes<VB, PAGED>(L, (f0.y & ~15u) + vo, v[1]);
-        load_bytes<VB, PAGED>(L, (f1.x & ~15u) + vo, v[2]);
-        load_bytes<VB, PAGED>(L, (f1.y & ~15u) + vo, v[3]);
+        auto load_v = [&]() {
+            const uint4 f0 = *reinterpret_cast<const uint4 *>(&tl.ent[c + 2 * t]);
+            const uint4 f1 = *reinterpret_cast<const uint4 *>(&tl.ent[c + 8 + 2 * t]);
+            const uint32_t vo = D * BITS / 8 + VB * g;
+            load_bytes<VB, PAGED>(L, (f0.x & ~15u) + vo, v[0]);
+            load_bytes<VB, PAGED>(L, (f0.z & ~15u) + vo, v[1]);
+            load_bytes<VB, PAGED>(L, (f1.x & ~15u) + vo, v[2]);
+            load_bytes<VB, PAGED>(L, (f1.z & ~15u) + vo, v[3]);
+        };
+        if (CLS != 3) load_v();
         // S^T: a word gives 16/BITS operand pairs of its key; equal fields share a sum (for wide codes
         // two sums alternate), so no chain of dependent instructions is longer than 4
         float sf[4][4];
@@ -276,15 +320,15 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
         for (int i = 0; i < 4; ++i) sf[i][0] = sf[i][1] = sf[i][2] = sf[i][3] = 0.f;
         if constexpr (CLS == 3) {
 #pragma unroll
-            for (int i = 0; i < KW; i += 2) mma(sf[i / 2 & 1], k0[i], k1[i], k0[i + 1], k1[i + 1], q[i], q[i + 1]);
+            for (int i = 0; i < KW; i += 2) mma(sf[i / 2 & 1], kr.a[i], kr.b[i], kr.a[i + 1], kr.b[i + 1], q[i], q[i + 1]);
         } else if constexpr (CLS == 2) {
 #pragma unroll
             for (int i = 0; i < KW; ++i)
-                mma(sf[i & 1], raw_field<8, 0>(k0[i]), raw_field<8, 0>(k1[i]), raw_field<8, 0>(k0[i] >> 8),
-                    raw_field<8, 0>(k1[i] >> 8), q[2 * i], q[2 * i + 1]);
+                mma(sf[i & 1], raw_field<8, 0>(kr.a[i]), raw_field<8, 0>(kr.b[i]), raw_field<8, 0>(kr.a[i] >> 8),
+                    raw_field<8, 0>(kr.b[i] >> 8), q[2 * i], q[2 * i + 1]);
         } else {
 #pragma unroll
-            for (int i = 0; i < KW; ++i) k_fields<BITS, 0>(sf, k0[i], k1[i], q + i * F);
+            for (int i = 0; i < KW; ++i) k_fields<BITS, 0>(sf, kr.a[i], kr.b[i], q + i * F);
         }
         float s[4];
 #pragma unroll
@@ -293,15 +337,22 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
             else if (CLS == 1) s[i] = fmaf(sf[1][i], 0.0625f, sf[0][i]);
             else s[i] = fmaf(fmaf(fmaf(sf[3][i], 0.25f, sf[2][i]), 0.25f, sf[1][i]), 0.25f, sf[0][i]);
         }
-        const float4 sd0 = tl.side[c + g], sd1 = tl.side[c + 8 + g];
-        const bool v0 = e0 & kValid, v1 = e1 & kValid;
+        // logits in log2 units: codes entered as c 2^-24
+        const float ka = CLS == 3 ? cdot : kr.sa.x * (cdot * 16777216.f), kb = CLS == 3 ? cdot : kr.sb.x * (cdot * 16777216.f);
+        const float za = CLS == 3 ? 0.f : kr.sa.y, zb = CLS == 3 ? 0.f : kr.sb.y;
+        const float sva = CLS == 3 ? 1.f : kr.sa.z, svb = CLS == 3 ? 1.f : kr.sb.z;
+        const float zva = CLS == 3 ? 0.f : fmaf(mid, kr.sa.z, kr.sa.w), zvb = CLS == 3 ? 0.f : fmaf(mid, kr.sb.z, kr.sb.w);
         float lg[4];
-        lg[0] = v0 && on0 ? fmaf(sd0.x, s[0], sd0.y * qs0) : -INFINITY;
-        lg[1] = v0 && on1 ? fmaf(sd0.x, s[1], sd0.y * qs1) : -INFINITY;
-        lg[2] = v1 && on0 ? fmaf(sd1.x, s[2], sd1.y * qs0) : -INFINITY;
-        lg[3] = v1 && on1 ? fmaf(sd1.x, s[3], sd1.y * qs1) : -INFINITY;
+        lg[0] = kr.va && on0 ? fmaf(ka, s[0], za * qs0) : -INFINITY;
+        lg[1] = kr.va && on1 ? fmaf(ka, s[1], za * qs1) : -INFINITY;
+        lg[2] = kr.vb && on0 ? fmaf(kb, s[2], zb * qs0) : -INFINITY;
+        lg[3] = kr.vb && on1 ? fmaf(kb, s[3], zb * qs1) : -INFINITY;
+        if (c + 16 * kWarps < end) kr.load(tl, L, side, c + 16 * kWarps, g, t);
+        if (CLS == 3) load_v();
         float mx0 = fmaxf(lg[0], lg[2]), mx1 = fmaxf(lg[1], lg[3]);
-        if (__any_sync(0xffffffffu, mx0 > st.m[0] + kLazy || mx1 > st.m[1] + kLazy)) {
+        const float smax = fmaxf(sva, svb);
+        // (the unit is raised before a scale reaches S = 2^11 units)
+        if (__any_sync(0xffffffffu, mx0 > st.m[0] + kLazy || mx1 > st.m[1] + kLazy || (CLS != 3 && smax > 2048.f * st.unit))) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
@@ -322,6 +373,10 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
                 st.o[i][2] *= c0;
                 st.o[i][3] *= c1;
             }
+            if (CLS != 3) {
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));
+                if (__uint_as_float(top) > 2048.f * st.unit) set_unit(st, top);
+            }
         }
         float p[4];
 #pragma unroll
@@ -329,10 +384,11 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
         st.l[0] += p[0] + p[2];
         st.l[1] += p[1] + p[3];
         if (CLS != 3) {
-            st.pz[0] = fmaf(p[0], sd0.w, fmaf(p[2], sd1.w, st.pz[0]));
-            st.pz[1] = fmaf(p[1], sd0.w, fmaf(p[3], sd1.w, st.pz[1]));
+            st.pz[0] = fmaf(p[0], zva, fmaf(p[2], zvb, st.pz[0]));
+            st.pz[1] = fmaf(p[1], zva, fmaf(p[3], zvb, st.pz[1]));
         }
-        const float w0 = CLS == 3 ? fac : sd0.z * fac, w1 = CLS == 3 ? fac : sd1.z * fac;
+        const float fac = __uint_as_float((254u << 23) - __float_as_uint(st.unit));    // 1 / unit, a power of two
+        const float w0 = CLS == 3 ? fac : sva * fac, w1 = CLS == 3 ? fac : svb * fac;
         p[0] *= w0;
         p[1] *= w0;
         p[2] *= w1;
@@ -387,7 +443,7 @@ struct Job {
 };
 
 template <int D, bool PAGED, int NQ>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 4)
 decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *__restrict__ out)
 {
     extern __shared__ __align__(16) uint8_t raw[];
@@ -427,23 +483,22 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         *reinterpret_cast<uint4 *>(&sm.rows[qi][8 * ch]) = v;
     }
     __syncthreads();
-#pragma unroll 1
-    for (int x = tid; x < 4 * (D / 32) * 32; x += kThreads) {
-        const int cls = x / (D / 32 * 32), i = x / 32 % (D / 32), ln = x % 32;
-        const int ch0 = (ln & 3) * (D / 4), fl = 3 - cls, f = 1 << fl;     // f = 16 / bits fields per half word
-        uint32_t r[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int p = 4 * i + e;             // operand pair: word p / f, field p % f
-            const __half *src = &sm.rows[(ln >> 2) & (NQ - 1)][ch0 + ((p >> fl) << (fl + 1)) + (p & (f - 1))];
-            const __half2 v = __halves2half2(src[0], src[f]);
-            r[e] = *reinterpret_cast<const uint32_t *>(&v);
-        }
-        sm.q[cls][i][ln] = make_uint4(r[0], r[1], r[2], r[3]);
+    // 16 bytes are four pairs (channel, channel + f), f = 16 / bits fields to a half word
+    for (int x = tid; x < (D / 32) * 32; x += kThreads) {
+        const int i = x / 32, ln = x % 32;
+        const __half *row = &sm.rows[(ln >> 2) & (NQ - 1)][(ln & 3) * (D / 4)];
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + 8 * i);
+        const uint2 va = *reinterpret_cast<const uint2 *>(row + (i >> 1) * 16 + (i & 1) * 4);
+        const uint2 vb = *reinterpret_cast<const uint2 *>(row + (i >> 1) * 16 + (i & 1) * 4 + 8);
+        sm.q[3][i][ln] = v;
+        sm.q[2][i][ln] = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                                    __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+        sm.q[1][i][ln] = make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+        sm.q[0][i][ln] = make_uint4(__byte_perm(va.x, vb.x, 0x5410), __byte_perm(va.x, vb.x, 0x7632),
+                                    __byte_perm(va.y, vb.y, 0x5410), __byte_perm(va.y, vb.y, 0x7632));
     }
-    static_assert(kWarps == kQ, "a warp sums one query");
-    {
-        const int qi = warp;
+    for (int qi = warp; qi < kQ; qi += kWarps) {
         float a = 0.f;
 #pragma unroll
         for (int ch = 0; ch < D; ch += 32) a += __half2float(sm.rows[qi & (NQ - 1)][ch + lane]);
@@ -462,9 +517,10 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         st.l[i] = st.pz[i] = 0.f;
     }
     st.unit = 1.f;
-    const float cdot = kLog2e / sqrtf((float)D);
     Tile &tl = sm.tile;
     const RecLoc L = rec_loc(c, s, h, 0);
+    const uint32_t *meta = c.meta + slot0;
+    const float4 *side = c.side + slot0;
     const int a0 = min(e_all, split * share), a1 = min(e_all, a0 + share);
     for (int a = a0; a < a1;) {
         // a tile: up to kTileKeys entries of one kind, the warps' parts multiples of 32
@@ -473,109 +529,104 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         const int per = ((n + kWarps - 1) / kWarps + 31) & ~31;
         const int p0 = warp * per, p1 = min(n, p0 + per);
         const uint32_t act = blocks ? full : local;
-        uint32_t mt[kSteps], bal[kSteps][4];
-        int64_t slot[kSteps];
+        const int bs = job.block_shift, x0 = (a >> bs) - 1;
+        if (blocks) {
+            for (int i = tid; i < kTileKeys / 16 + 2; i += kThreads) {
+                const int x = x0 + i;
+                sm.ids[i] = x >= 0 && x < job.k ? job.ids[(int64_t)sh * job.k + x] : -1;
+            }
+        }
+        __syncthreads();
+        uint32_t mt[kSteps];
+        int js[kSteps];
         int cnt[4] = {0, 0, 0, 0};
-        if (tid < 4) sm.smax[tid] = 0u;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             mt[i] = 0;
-            slot[i] = slot0;
+            js[i] = -1;
             const int e = a + p0 + i * 32 + lane;
             if (p0 + i * 32 >= p1) continue;
-            int j = -1;
             if (e < a + p1) {
                 if (blocks) {
-                    const int x = e >> job.block_shift;
-                    const int id = x < job.k ? job.ids[(int64_t)sh * job.k + x] : -1;
+                    const int x = e >> bs, id = sm.ids[x - x0], before = sm.ids[x - x0 - 1];
                     if (id >= 0) {
-                        const int before = x > 0 ? job.ids[(int64_t)sh * job.k + x - 1] : -1;
                         if ((x > 0 && before < 0) || id <= before || id >= nb) {
                             set_status(c.status, KVQ_ERR_DEVICE_CHECK);
                         } else {
-                            j = (id << job.block_shift) + (e & ((1 << job.block_shift) - 1));
-                            if (j >= len) j = -1;
+                            const int j = (id << bs) + (e & ((1 << bs) - 1));
+                            if (j < len) js[i] = j;
                         }
                     }
                 } else {
-                    j = len - wl + e - e_block;
+                    js[i] = len - wl + e - e_block;
                 }
             }
-            if (j >= 0) {
-                slot[i] = slot0 + j;
-                mt[i] = c.meta[slot[i]] | kValid;
-            }
+            if (js[i] >= 0) mt[i] = meta[js[i]] | kValid;
         }
         // 16 consecutive entries are consecutive keys, the valid ones in front: ask for their
         // side entries and records
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) bal[i][w] = 0u;
             if (p0 + i * 32 >= p1) continue;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                bal[i][w] = __ballot_sync(0xffffffffu, (mt[i] & 7u) == (kValid | w));
-                cnt[w] += __popc(bal[i][w]);
-            }
-            const uint32_t ok = bal[i][0] | bal[i][1] | bal[i][2] | bal[i][3];
-            const int hb = lane & 16, keys = __popc((ok >> hb) & 0xFFFFu);
+            const uint32_t v = __ballot_sync(0xffffffffu, mt[i] & kValid), b0 = __ballot_sync(0xffffffffu, mt[i] & 1u),
+                           b1 = __ballot_sync(0xffffffffu, mt[i] & 2u);
+            cnt[0] += __popc(v & ~b0 & ~b1);
+            cnt[1] += __popc(b0 & ~b1);
+            cnt[2] += __popc(b1 & ~b0);
+            cnt[3] += __popc(b0 & b1);
+            const int hb = lane & 16, keys = __popc((v >> hb) & 0xFFFFu);
             const uint32_t last = __shfl_sync(0xffffffffu, mt[i], hb + max(keys - 1, 0));
             if (lane == hb && keys > 0) {
-                prefetch_l2(&c.side[slot[i]], 16u * keys);
+                prefetch_l2(side + js[i], 16u * keys);
                 prefetch_records<PAGED>(L, mt[i] & ~15u, (last & ~15u) + ((uint32_t)(D / 2) << (last & 3u)));
             }
         }
         if (lane < 4) sm.cnt[warp][lane] = lane == 0 ? cnt[0] : lane == 1 ? cnt[1] : lane == 2 ? cnt[2] : cnt[3];
         __syncthreads();
-        // slots: width by width, each width's keys in the warps' order, padded to 16
+        // slots: width by width, each width's keys in the warps' order, padded to 16. Lane
+        // 4 x + w holds warp x's count of width w; sums over the warps, then over the widths
         int all[4], at[4], first[5];
-        first[0] = 0;
+        {
+            const int mine = lane < 4 * kWarps ? sm.cnt[lane >> 2][lane & 3] : 0;
+            int upto = mine;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            all[w] = 0;
-            at[w] = 0;
-#pragma unroll
-            for (int x = 0; x < kWarps; ++x) {
-                const int m = sm.cnt[x][w];
-                if (x < warp) at[w] += m;
-                all[w] += m;
+            for (int d = 4; d < 4 * kWarps; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += y;
             }
-            at[w] += first[w];
-            first[w + 1] = first[w] + ((all[w] + 15) & ~15);
+            first[0] = 0;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                all[w] = __shfl_sync(0xffffffffu, upto, 4 * (kWarps - 1) + w);
+                at[w] = first[w] + __shfl_sync(0xffffffffu, upto - mine, 4 * warp + w);
+                first[w + 1] = first[w] + ((all[w] + 15) & ~15);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             if (p0 + i * 32 >= p1) continue;
+            const uint32_t v = __ballot_sync(0xffffffffu, mt[i] & kValid), b0 = __ballot_sync(0xffffffffu, mt[i] & 1u),
+                           b1 = __ballot_sync(0xffffffffu, mt[i] & 2u);
             const int w = mt[i] & 3;
-            const uint32_t b = w == 0 ? bal[i][0] : w == 1 ? bal[i][1] : w == 2 ? bal[i][2] : bal[i][3];
-            const int to = w == 0 ? at[0] : w == 1 ? at[1] : w == 2 ? at[2] : at[3];
-            float4 sd = make_float4(0.f, 0.f, 0.f, 0.f);
             if (mt[i] & kValid) {
-                sd = __ldg(&c.side[slot[i]]);
-                const int pos = to + __popc(b & ((1u << lane) - 1u));
-                const float mid = w == 3 ? 0.f : (float)(1 << ((2 << w) - 1));
-                tl.ent[pos] = mt[i];
-                tl.side[pos] = make_float4(sd.x * (w == 3 ? cdot : cdot * 16777216.f), sd.y * cdot, sd.z, fmaf(mid, sd.z, sd.w));
-                sm.some[w] = mt[i];               // any one of them
+                const uint32_t own = v & (w & 1 ? b0 : ~b0) & (w & 2 ? b1 : ~b1);
+                const int to = w & 2 ? (w & 1 ? at[3] : at[2]) : (w & 1 ? at[1] : at[0]);
+                const uint2 ent = make_uint2(mt[i], (uint32_t)js[i]);
+                tl.ent[to + __popc(own & ((1u << lane) - 1u))] = ent;
+                sm.some[w] = ent;                 // any one of them
             }
-#pragma unroll
-            for (int x = 0; x < 3; ++x) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, w == x ? __float_as_uint(sd.z) : 0u);
-                if (lane == 0 && bal[i][x]) atomicMax(&sm.smax[x], top);
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) at[x] += __popc(bal[i][x]);
+            at[0] += __popc(v & ~b0 & ~b1);
+            at[1] += __popc(b0 & ~b1);
+            at[2] += __popc(b1 & ~b0);
+            at[3] += __popc(b0 & b1);
         }
         __syncthreads();
         // padding up to 16: a real record's offset, no kValid
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             const int to = first[w] + all[w] + lane;
-            if (warp == w && all[w] > 0 && to < first[w + 1]) {
-                tl.ent[to] = sm.some[w] & ~kValid;
-                tl.side[to] = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            if (warp == w && all[w] > 0 && to < first[w + 1])
+                tl.ent[to] = make_uint2(sm.some[w].x & ~kValid, sm.some[w].y);
         }
         __syncthreads();
         const bool on0 = (act >> (2 * t & (NQ - 1))) & 1u, on1 = (act >> ((2 * t & (NQ - 1)) + 1)) & 1u;
@@ -584,28 +635,10 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         for (int w = 0; w < 4; ++w) {
             const int b0 = first[w] + ((warp - first[w] / 16) & (kWarps - 1)) * 16, b1 = first[w + 1];
             if (b0 >= b1) continue;
-            // weights in units of S / 64, S a power of two above the largest scale (1 for fp16 values)
-            float fac = 64.f, unit = 0.015625f;
-            if (w != 3) {
-                const int e = min(max((int)(sm.smax[w] >> 23) + 1, 87), 167);     // biased exponent of S
-                unit = __uint_as_float((uint32_t)(e - 6) << 23);
-                fac = __uint_as_float((uint32_t)(254 - e + 6) << 23);
-            }
-            if (unit != st.unit) {
-                const float r = st.unit / unit;  // a power of two: exact
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    st.o[i][0] *= r;
-                    st.o[i][1] *= r;
-                    st.o[i][2] *= r;
-                    st.o[i][3] *= r;
-                }
-                st.unit = unit;
-            }
-            if (w == 0) run_class<D, 0, PAGED, NQ>(st, sm, L, b0, b1, fac, on0, on1);
-            else if (w == 1) run_class<D, 1, PAGED, NQ>(st, sm, L, b0, b1, fac, on0, on1);
-            else if (w == 2) run_class<D, 2, PAGED, NQ>(st, sm, L, b0, b1, fac, on0, on1);
-            else run_class<D, 3, PAGED, NQ>(st, sm, L, b0, b1, fac, on0, on1);
+            if (w == 0) run_class<D, 0, PAGED, NQ>(st, sm, L, side, b0, b1, on0, on1);
+            else if (w == 1) run_class<D, 1, PAGED, NQ>(st, sm, L, side, b0, b1, on0, on1);
+            else if (w == 2) run_class<D, 2, PAGED, NQ>(st, sm, L, side, b0, b1, on0, on1);
+            else run_class<D, 3, PAGED, NQ>(st, sm, L, side, b0, b1, on0, on1);
         }
         a += n;
         __syncthreads();                         // the tile's slots are read; the next one overwrites them
@@ -620,23 +653,19 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
             st.pz[i] += __shfl_xor_sync(0xffffffffu, st.pz[i], d);
         }
     }
-    if (NQ == 4) {                               // the rests join their queries
-#pragma unroll
-        for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st.o[mt][i] += __shfl_down_sync(0xffffffffu, st.o[mt][i], 2);
-    }
-    if (2 * t < nq) {
+    // columns 4..7 of up to 4 queries are the weights' second parts: left as states of their own
+    if (2 * (t & (NQ / 2 - 1)) < nq) {
         const int g = lane >> 2;
+        const bool rest = 2 * t >= NQ;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float *o = sm.o[warp][2 * t + i];
+            const float add = rest ? 0.f : st.pz[i];
 #pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) {
-                o[g * (D / 8) + 2 * mt] = fmaf(st.o[mt][i], st.unit, st.pz[i]);
-                o[g * (D / 8) + 2 * mt + 1] = fmaf(st.o[mt][2 + i], st.unit, st.pz[i]);
-            }
-            if (g == 0) {
+            for (int mt = 0; mt < D / 16; ++mt)
+                *reinterpret_cast<float2 *>(&o[g * (D / 8) + 2 * mt]) =
+                    make_float2(fmaf(st.o[mt][i], st.unit, add), fmaf(st.o[mt][2 + i], st.unit, add));
+            if (g == 0 && !rest) {
                 o[D] = st.m[i];
                 o[D + 1] = st.l[i];
             }
@@ -653,7 +682,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         for (int wp = 0; wp < kWarps; ++wp) {
             const float f = ex2(sm.o[wp][qi][D] - M);
             l = fmaf(sm.o[wp][qi][D + 1], f, l);
-            o = fmaf(sm.o[wp][qi][ch], f, o);
+            o = fmaf(sm.o[wp][qi][ch] + (NQ == 4 ? sm.o[wp][qi + 4][ch] : 0.f), f, o);
         }
         if (job.n_split == 1) {
             out[(q0 + qi) * D + ch] = l > 0.f ? o / l : 0.f;
@@ -741,7 +770,7 @@ int splits(const kvq_cache *cache, int k, int block, int w)
     const int64_t keys_b = std::min<int64_t>((int64_t)k * block, ((int64_t)cache->max_cap + block - 1) / block * block);
     const int64_t keys_w = std::min<int64_t>((int64_t)w + 1, cache->max_cap);
     const int64_t keys = c.G == 1 ? std::max(keys_b, keys_w) : keys_b + keys_w;
-    const int64_t want = ((int64_t)num_sms() + units - 1) / units;
+    const int64_t want = (2 * (int64_t)num_sms() + units - 1) / units;
     return (int)std::max<int64_t>(1, std::min<int64_t>(want, (keys + 64 * kWarps - 1) / (64 * kWarps)));
 }
 
@@ -754,6 +783,10 @@ cudaError_t launch_typed(const kvq_cache *cache, const __half *q, const Job &job
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)c.B * c.H * job.n_sub;
     const dim3 grid((unsigned)(units * job.n_split));
+    if (job.n_split > 8 && job.n_split <= kMaxCluster) {
+        e = ensure_cluster_attr((const void *)decode_blocks_kernel<D, PAGED, NQ>);
+        if (e != cudaSuccess) return e;
+    }
     if (job.n_split > 1 && job.n_split <= kMaxCluster) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;

@@ -406,6 +406,8 @@ int num_sms();
 // Raise `func`'s dynamic shared-memory limit to `bytes` on the current device; done once
 // per (kernel, device), thread-safe.
 cudaError_t ensure_smem_attr(const void *func, size_t bytes);
+// Allow `func` clusters of up to 16 CTAs on the current device; as above.
+cudaError_t ensure_cluster_attr(const void *func);
 // records a host-side status for kvq_last_error() and returns `code`
 int report_error(int code, const char *msg);
 // profiling hook (kvq_set_profile_events): record the caller's events around a main kernel
