@@ -21,18 +21,94 @@ constexpr int kTile = KVQ_BLOCK_TILE;    // blocks per tile of the bounds layout
 
 // ------------------------------------------------------------------ bounds
 // A CTA takes groups of kGroup blocks of one (sequence, head): their 32-byte rows of the
-// layout are whole sectors. Each block is cut into kSubs runs of keys, a run per warp at a
-// time: D/4 lanes per key, 4 channels per lane. The runs' minima and maxima meet in shared
-// memory as fp16.
-constexpr int kBThreads = 256, kGroup = 16, kSubs = 4;
+// layout are whole sectors. A warp takes a run of up to 64 keys at a time, a whole block (half a
+// one of 128) when the group has a block for every warp, else a quarter of one: it sorts the run's keys by width, asks for
+// their records, then takes D/16 lanes per key, 16 channels per lane (two steps' loads in flight
+// for the narrow widths: four cost more in code than they hide). A field at bit p joins the mantissa of m = 2^(23 - p), whose last place there is 1, and
+// one fused multiply-add takes it to fl((m + c) s - m s) = fl(c s), m s being exact. The runs'
+// minima and maxima meet in shared memory as fp16.
+constexpr int kBThreads = 256, kBWarps = kBThreads / 32, kGroup = 16, kMaxSubs = 4, kMaxRun = 64;
 
 template <int D>
-__global__ void __launch_bounds__(kBThreads)
+struct BoundsSmem {
+    // per run of the group: lo and hi, padded
+    __half part[kMaxSubs * kBWarps][2 * D + 2];
+    uint4 ent[kBWarps][kMaxRun];                               // a run's keys by width: offset, s, z
+};
+
+// lo and hi over the n keys of `ent`, all of width 2 << CLS; gk, li: the lane's key of a step and
+// its 16 channels. A last step's missing keys repeat the last one, which changes nothing.
+template <int D, int CLS, bool PAGED>
+__device__ __forceinline__ void bounds_class(__half2 (&lo)[8], __half2 (&hi)[8], const RecLoc &L, const uint4 *ent, int n, int gk,
+                                             int li)
+{
+    constexpr int BITS = 2 << CLS, KPW = 512 / D, W = BITS / 2;      // W words of 16 codes
+    constexpr int kFly = CLS >= 2 ? 1 : 2;
+    for (int i0 = 0; i0 < n; i0 += kFly * KPW) {
+        uint32_t w[kFly][W];
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const uint32_t off = ent[min(i0 + f * KPW + gk, n - 1)].x + 2 * BITS * li;
+            const uint8_t *p = PAGED ? L.at(off) : L.base + off;
+            if (CLS == 0) {
+                w[f][0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+            } else if (CLS == 1) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+                w[f][0] = v.x;
+                w[f][1 % W] = v.y;
+            } else {
+#pragma unroll
+                for (int x = 0; x < W / 4; ++x) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(PAGED && x ? L.at(off + 16 * x) : p + 16 * x));
+                    w[f][4 * x % W] = v.x;
+                    w[f][(4 * x + 1) % W] = v.y;
+                    w[f][(4 * x + 2) % W] = v.z;
+                    w[f][(4 * x + 3) % W] = v.w;
+                }
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            if (f > 0 && i0 + f * KPW >= n) break;
+            const uint4 en = ent[min(i0 + f * KPW + gk, n - 1)];
+            const float sc = __uint_as_float(en.y), z = __uint_as_float(en.z);
+            // P fields at bits 0, BITS, .. of a word shifted down by SH at a time
+            constexpr int P = CLS == 2 ? 2 : 4, SH = P * BITS, N = CLS == 3 ? 1 : P;
+            float ms[N];                                       // -m s by position
+            if constexpr (CLS != 3) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) ms[i] = sc * __uint_as_float(0xCB000000u - ((uint32_t)(i * BITS) << 23));
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                __half2 x;
+                if constexpr (CLS == 3) {
+                    x = *reinterpret_cast<const __half2 *>(&w[f][e / 2]);
+                } else {
+                    const uint32_t v = w[f][e * BITS / 32] >> ((e * BITS & 31) / SH * SH);
+                    constexpr uint32_t one = (1u << BITS) - 1u;
+                    const int i = e % P;
+                    const uint32_t c0 = (v & (one << (i * BITS))) | (0x4B000000u - ((uint32_t)(i * BITS) << 23));
+                    const uint32_t c1 = (v & (one << (i * BITS + BITS))) | (0x4B000000u - ((uint32_t)(i * BITS + BITS) << 23));
+                    const float2 y = __fadd2_rn(__ffma2_rn(make_float2(__uint_as_float(c0), __uint_as_float(c1)), make_float2(sc, sc),
+                                                           make_float2(ms[i % N], ms[(i + 1) % N])),
+                                                make_float2(z, z));
+                    x = __floats2half2_rn(y.x, y.y);
+                }
+                lo[e / 2] = __hmin2(lo[e / 2], x);
+                hi[e / 2] = __hmax2(hi[e / 2], x);
+            }
+        }
+    }
+}
+
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(kBThreads, 4)
 bounds_kernel(CacheView c, int block, const int32_t *__restrict__ cu, __half *__restrict__ bounds, int nt, int per_sh)
 {
-    constexpr int LPK = D / 4, KPW = 32 / LPK;                 // lanes per key, keys per warp step
-    constexpr int ROW = kSubs * 2 * D + 2;                     // one block's partials, padded
-    __shared__ __half part[kGroup * ROW];
+    constexpr int LPK = D / 16;                                // lanes per key
+    extern __shared__ __align__(16) uint8_t raw[];
+    BoundsSmem<D> &sm = *reinterpret_cast<BoundsSmem<D> *>(raw);
     pdl_wait();
     pdl_trigger();
     const int sh = blockIdx.x / per_sh, s = sh / c.H, h = sh % c.H;
@@ -49,69 +125,117 @@ bounds_kernel(CacheView c, int block, const int32_t *__restrict__ cu, __half *__
     }
     const int b_lo = first / block, b_hi = (len + block - 1) / block;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane % LPK, gk = lane / LPK;
-    const int run = block / kSubs;
     const int64_t slot0 = slot_of(c, s, h, 0);
+    const RecLoc L = rec_loc(c, s, h, 0);
+    uint4 *ent = sm.ent[warp];
+    const uint32_t below = (1u << lane) - 1u;
     for (int g = b_lo / kGroup + blockIdx.x % per_sh; g * kGroup < b_hi; g += per_sh) {
         const int b0 = max(b_lo, g * kGroup), b1 = min(b_hi, (g + 1) * kGroup);
-        for (int u = warp; u < (b1 - b0) * kSubs; u += kBThreads / 32) {
-            const int b = b0 + u / kSubs, sub = u % kSubs;
+        const int subs = b1 - b0 < kBWarps ? kMaxSubs : block > kMaxRun ? block / kMaxRun : 1, run = block / subs;
+        for (int u = warp; u < (b1 - b0) * subs; u += kBWarps) {
+            const int b = b0 + u / subs, sub = u % subs;
             const int j0 = b * block + sub * run, n = min(run, len - j0);      // n <= 0: an empty run
-            uint32_t mt = 0;
-            float2 sd = make_float2(1.f, 0.f);
-            if (lane < n) {
-                mt = c.meta[slot0 + j0 + lane];
-                sd = *reinterpret_cast<const float2 *>(&c.side[slot0 + j0 + lane]);
-            }
-            float lo[4], hi[4];
+            __half2 lo[8], hi[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                lo[e] = INFINITY;
-                hi[e] = -INFINITY;
+            for (int e = 0; e < 8; ++e) {
+                lo[e] = __half2half2(__ushort_as_half(0x7C00));                // +inf, -inf
+                hi[e] = __half2half2(__ushort_as_half(0xFC00));
             }
-            for (int i0 = 0; i0 < n; i0 += KPW) {
-                const int i = i0 + gk;
-                const uint32_t m = __shfl_sync(0xffffffffu, mt, i & 31);
-                const float sc = __shfl_sync(0xffffffffu, sd.x, i & 31), z = __shfl_sync(0xffffffffu, sd.y, i & 31);
-                if (i >= n) continue;
-                const int wc = (int)(m & 3u);
-                const RecLoc L = rec_loc(c, s, h, m & ~15u);
-                const uint8_t *p = L.at((uint32_t)(li << wc));                 // 4 channels: 1, 2, 4 or 8 bytes
-                float x[4];
-                if (wc == 0) code_values<0, 4>(make_uint2(*p, 0u), sc, z, x);
-                else if (wc == 1) code_values<1, 4>(make_uint2(*reinterpret_cast<const uint16_t *>(p), 0u), sc, z, x);
-                else if (wc == 2) code_values<2, 4>(make_uint2(*reinterpret_cast<const uint32_t *>(p), 0u), sc, z, x);
-                else code_values<3, 4>(*reinterpret_cast<const uint2 *>(p), sc, z, x);
+            // the run's keys by width: counts, then places
+            constexpr uint32_t kKey = 4u;                                      // (offsets are multiples of 16)
+            uint32_t mt[kMaxRun / 32];
+            float2 sd[kMaxRun / 32];
+            int cnt[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    lo[e] = fminf(lo[e], x[e]);
-                    hi[e] = fmaxf(hi[e], x[e]);
+            for (int i = 0; i < kMaxRun / 32; ++i) {
+                const int j = i * 32 + lane;
+                mt[i] = 0u;
+                if (j < n) {
+                    mt[i] = c.meta[slot0 + j0 + j] | kKey;
+                    sd[i] = *reinterpret_cast<const float2 *>(&c.side[slot0 + j0 + j]);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < kMaxRun / 32; ++i) {
+                if (i * 32 >= n) continue;
+                if (mt[i] & kKey) {
+                    const uint32_t off = mt[i] & ~15u, bytes = (uint32_t)(D / 4) << (mt[i] & 3u);
+                    for (uint32_t o = 0; o < bytes; o += 64) {
+                        const uint8_t *p = PAGED ? L.at(off + o) : L.base + off + o;
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+                    }
+                }
+                const uint32_t v = __ballot_sync(0xffffffffu, mt[i] & kKey), w0 = __ballot_sync(0xffffffffu, mt[i] & 1u),
+                               w1 = __ballot_sync(0xffffffffu, mt[i] & 2u);
+                cnt[0] += __popc(v & ~w0 & ~w1);
+                cnt[1] += __popc(w0 & ~w1);
+                cnt[2] += __popc(w1 & ~w0);
+                cnt[3] += __popc(w0 & w1);
+            }
+            int at[4] = {0, cnt[0], cnt[0] + cnt[1], cnt[0] + cnt[1] + cnt[2]};
+#pragma unroll
+            for (int i = 0; i < kMaxRun / 32; ++i) {
+                if (i * 32 >= n) continue;
+                const uint32_t v = __ballot_sync(0xffffffffu, mt[i] & kKey), w0 = __ballot_sync(0xffffffffu, mt[i] & 1u),
+                               w1 = __ballot_sync(0xffffffffu, mt[i] & 2u);
+                if (mt[i] & kKey) {
+                    const uint32_t own = v & (mt[i] & 1u ? w0 : ~w0) & (mt[i] & 2u ? w1 : ~w1);
+                    const int to = mt[i] & 2u ? (mt[i] & 1u ? at[3] : at[2]) : (mt[i] & 1u ? at[1] : at[0]);
+                    ent[to + __popc(own & below)] = make_uint4(mt[i] & ~15u, __float_as_uint(sd[i].x), __float_as_uint(sd[i].y), 0u);
+                }
+                at[0] += __popc(v & ~w0 & ~w1);
+                at[1] += __popc(w0 & ~w1);
+                at[2] += __popc(w1 & ~w0);
+                at[3] += __popc(w0 & w1);
+            }
+            __syncwarp();
+            const uint4 *e0 = ent, *e1 = e0 + cnt[0], *e2 = e1 + cnt[1], *e3 = e2 + cnt[2];
+            if (cnt[0]) bounds_class<D, 0, PAGED>(lo, hi, L, e0, cnt[0], gk, li);
+            if (cnt[1]) bounds_class<D, 1, PAGED>(lo, hi, L, e1, cnt[1], gk, li);
+            if (cnt[2]) bounds_class<D, 2, PAGED>(lo, hi, L, e2, cnt[2], gk, li);
+            if (cnt[3]) bounds_class<D, 3, PAGED>(lo, hi, L, e3, cnt[3], gk, li);
+            __syncwarp();
 #pragma unroll
             for (int d = LPK; d < 32; d <<= 1) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    lo[e] = fminf(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
-                    hi[e] = fmaxf(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
+                for (int e = 0; e < 8; ++e) {
+                    lo[e] = __hmin2(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
+                    hi[e] = __hmax2(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
                 }
             }
             if (gk == 0) {
-                __half2 *dst = reinterpret_cast<__half2 *>(part + (b - g * kGroup) * ROW + sub * 2 * D + 4 * li);
-                dst[0] = __floats2half2_rn(lo[0], lo[1]);
-                dst[1] = __floats2half2_rn(lo[2], lo[3]);
-                dst[D / 2] = __floats2half2_rn(hi[0], hi[1]);
-                dst[D / 2 + 1] = __floats2half2_rn(hi[2], hi[3]);
+                __half2 *dst = reinterpret_cast<__half2 *>(&sm.part[(b - b0) * subs + sub][16 * li]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dst[e] = lo[e];
+                    dst[D / 2 + e] = hi[e];
+                }
             }
         }
         __syncthreads();
-        for (int t = threadIdx.x; t < 2 * D * kGroup; t += kBThreads) {
-            const int bi = t % kGroup, b = g * kGroup + bi, mc = t / kGroup;    // mc: [lo/hi][channel]
-            if (b < b0 || b >= b1) continue;
-            const __half *p = part + bi * ROW + mc;
-            __half r = p[0];
+        if (b1 - b0 == kGroup && subs == 1) {
+            // a thread per row: the group's 16 blocks are one 32-byte sector of it
+            for (int mc = threadIdx.x; mc < 2 * D; mc += kBThreads) {
+                uint32_t w[kGroup / 2];
 #pragma unroll
-            for (int q = 1; q < kSubs; ++q) r = mc < D ? __hmin(r, p[q * 2 * D]) : __hmax(r, p[q * 2 * D]);
-            bounds[(((int64_t)sh * nt + b / kTile) * 2 * D + mc) * kTile + b % kTile] = r;
+                for (int i = 0; i < kGroup / 2; ++i) {
+                    const __half2 v = __halves2half2(sm.part[2 * i][mc], sm.part[2 * i + 1][mc]);
+                    // -0 and +0 are one value, stored as +0
+                    const __half2 z = __hadd2(v, __half2half2(__ushort_as_half(0)));
+                    w[i] = *reinterpret_cast<const uint32_t *>(&z);
+                }
+                uint4 *dst = reinterpret_cast<uint4 *>(bounds + (((int64_t)sh * nt + b0 / kTile) * 2 * D + mc) * kTile + b0 % kTile);
+                dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        } else {
+            for (int t = threadIdx.x; t < 2 * D * (b1 - b0); t += kBThreads) {
+                const int b = b0 + t / (2 * D), mc = t % (2 * D);               // mc: [lo/hi][channel]
+                const __half *p = &sm.part[(b - b0) * subs][mc];
+                __half r = p[0];
+                for (int q = 1; q < subs; ++q) r = mc < D ? __hmin(r, p[q * (2 * D + 2)]) : __hmax(r, p[q * (2 * D + 2)]);
+                bounds[(((int64_t)sh * nt + b / kTile) * 2 * D + mc) * kTile + b % kTile] = __hadd(r, __ushort_as_half(0));
+            }
         }
         __syncthreads();
     }
@@ -133,67 +257,80 @@ __device__ __forceinline__ double half_field(uint32_t top)     // the fp16 bits 
     return __hiloint2double((int)((uint32_t)((int32_t)top >> 6) & 0x81FFFC00u), 0);
 }
 
-// One CTA per (sequence, KV head, tile of 64 blocks). Lane = (channel mod 4, group of 8
-// blocks): a 16-byte load covers 8 blocks of a channel, a warp's load 4 channels.
+// The scores of tiles [t0, t1) of 64 blocks of one (sequence, KV head), by a CTA. Two tiles at a
+// time when there are two (half the warps each), else one. Lane = (channel mod 4, group of 8
+// blocks): a 16-byte load covers 8 blocks of a channel, a warp's load 4 channels. Scores go to
+// `dst`, and to `keep` (shared memory, blocks t0 * 64 on) when given.
 template <int D, int NQ>
-__global__ void __launch_bounds__(kSThreads)
-score_kernel(CacheView c, const __half *__restrict__ q, const __half *__restrict__ bounds,
-             const uint8_t *__restrict__ modes, int block, int nt, float *__restrict__ scores)
+struct ScoreSmem {
+    double qs[NQ][D];
+    double sum[kSWarps][NQ][kTile];
+    int act[64], n_act;
+};
+
+template <int D, int NQ>
+__device__ __forceinline__ void score_tiles(const CacheView &c, const __half *__restrict__ q, const __half *__restrict__ bounds,
+                                            const uint8_t *__restrict__ modes, int sh, int nb, int nt, int t0, int t1,
+                                            float *__restrict__ dst, float *keep, ScoreSmem<D, NQ> &sm)
 {
-    __shared__ double qs[NQ][D];
-    __shared__ double sum[kSWarps][NQ][kTile];
-    __shared__ int act[64], n_act;
-    pdl_wait();
-    pdl_trigger();
-    const int sh = blockIdx.x / nt, tile = blockIdx.x % nt, s = sh / c.H, h = sh % c.H;
-    const int nb = (c.len[sh] + block - 1) / block;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane >> 3, b8 = lane & 7;
-    const int64_t q0 = ((int64_t)s * c.H + h) * c.G;
-    if (tid == 0) {
+    const int64_t q0 = (int64_t)sh * c.G;
+    if (warp == 0) {                             // the group's full queries
         int n = 0;
-        for (int g = 0; g < c.G; ++g) {
-            const int m = modes ? modes[q0 + g] : KVQ_MODE_FULL;
-            if (m > 2) set_status(c.status, KVQ_ERR_MODE);
-            if (m == KVQ_MODE_FULL) act[n++] = g;
+        for (int g0 = 0; g0 < c.G; g0 += 32) {
+            const int g = g0 + lane;
+            int m = KVQ_MODE_SKIP;
+            if (g < c.G) {
+                m = modes ? modes[q0 + g] : KVQ_MODE_FULL;
+                if (m > 2) set_status(c.status, KVQ_ERR_MODE);
+            }
+            const uint32_t in = __ballot_sync(0xffffffffu, m == KVQ_MODE_FULL);
+            if (m == KVQ_MODE_FULL) sm.act[n + __popc(in & ((1u << lane) - 1u))] = g;
+            n += __popc(in);
         }
-        n_act = n;
+        if (lane == 0) sm.n_act = n;
     }
     __syncthreads();
-    float *dst = scores + ((int64_t)sh * nt + tile) * kTile;
-    const int here = min(kTile, nb - tile * kTile);            // blocks of this tile
-    float best = -INFINITY;
-    if (here > 0) {
+    const int n_act = sm.n_act;
+    for (int t = t0; t < t1; t += 2) {
+        const int pair = t + 1 < t1 ? 2 : 1, wpt = kSWarps / pair;     // warps per tile
+        const int tile = t + warp / wpt, w0 = warp % wpt;
         const uint4 *lo = reinterpret_cast<const uint4 *>(bounds + ((int64_t)sh * nt + tile) * 2 * D * kTile);
         const uint4 *hi = lo + D * (kTile / 8);
+        const bool some = nb > tile * kTile;                   // (otherwise nothing of the tile is read)
+        float best = -INFINITY;
         for (int a0 = 0; a0 < n_act; a0 += NQ) {
             const int n = min(NQ, n_act - a0);
-            for (int t = tid; t < NQ * D; t += kSThreads)
-                qs[t / D][t % D] = t / D < n ? (double)__half2float(q[(q0 + act[a0 + t / D]) * D + t % D]) * kQUp : 0.0;
-            __syncthreads();
+            if (t == t0 || n_act > NQ) {
+                for (int x = tid; x < NQ * D; x += kSThreads)
+                    sm.qs[x / D][x % D] = x / D < n ? (double)__half2float(q[(q0 + sm.act[a0 + x / D]) * D + x % D]) * kQUp : 0.0;
+                __syncthreads();
+            }
             double acc[NQ][8];
 #pragma unroll
             for (int g = 0; g < NQ; ++g)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[g][e] = 0.0;
+            if (some) {
 #pragma unroll 4
-            for (int i = 0; i < D / (4 * kSWarps); ++i) {
-                const int ch = (i * kSWarps + warp) * 4 + sub;
-                uint4 l, u;
-                if (NQ == 1) {
-                    l = u = (qs[0][ch] < 0.0 ? lo : hi)[ch * (kTile / 8) + b8];
-                } else {
-                    l = lo[ch * (kTile / 8) + b8];
-                    u = hi[ch * (kTile / 8) + b8];
-                }
-                const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, uw[4] = {u.x, u.y, u.z, u.w};
+                for (int ch = w0 * 4 + sub; ch < D; ch += 4 * wpt) {
+                    uint4 l, u;
+                    if (NQ == 1) {
+                        l = u = __ldg((sm.qs[0][ch] < 0.0 ? lo : hi) + ch * (kTile / 8) + b8);
+                    } else {
+                        l = __ldg(lo + ch * (kTile / 8) + b8);
+                        u = __ldg(hi + ch * (kTile / 8) + b8);
+                    }
+                    const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int g = 0; g < NQ; ++g) {
-                    const double qv = qs[g][ch];
+                    for (int g = 0; g < NQ; ++g) {
+                        const double qv = sm.qs[g][ch];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t w = NQ == 1 ? uw[e] : (qv < 0.0 ? lw[e] : uw[e]);
-                        acc[g][2 * e] = fma(qv, half_field(w << 16), acc[g][2 * e]);
-                        acc[g][2 * e + 1] = fma(qv, half_field(w), acc[g][2 * e + 1]);
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t w = NQ == 1 ? uw[e] : (qv < 0.0 ? lw[e] : uw[e]);
+                            acc[g][2 * e] = fma(qv, half_field(w << 16), acc[g][2 * e]);
+                            acc[g][2 * e + 1] = fma(qv, half_field(w), acc[g][2 * e + 1]);
+                        }
                     }
                 }
             }
@@ -204,30 +341,33 @@ score_kernel(CacheView c, const __half *__restrict__ q, const __half *__restrict
                     double v = acc[g][e];
                     v += __shfl_xor_sync(0xffffffffu, v, 8);
                     v += __shfl_xor_sync(0xffffffffu, v, 16);
-                    if (sub == 0) sum[warp][g][b8 * 8 + e] = v;
+                    if (sub == 0) sm.sum[warp][g][b8 * 8 + e] = v;
                 }
             __syncthreads();
-            if (tid < kTile) {
+            if (tid < pair * kTile) {
                 for (int g = 0; g < n; ++g) {
                     double v = 0.0;
-#pragma unroll
-                    for (int w = 0; w < kSWarps; ++w) v += sum[w][g][tid];
+                    for (int w = 0; w < wpt; ++w) v += sm.sum[tid / kTile * wpt + w][g][tid % kTile];
                     best = fmaxf(best, (float)(v * 256.0));
                 }
             }
             __syncthreads();
         }
+        if (tid < pair * kTile) {
+            const int b = t * kTile + tid;
+            const float v = b < nb ? best : -INFINITY;
+            dst[b] = v;
+            if (keep) keep[b - t0 * kTile] = v;
+        }
     }
-    if (tid < kTile) dst[tid] = tid < here ? best : -INFINITY;
 }
 
 // ------------------------------------------------------------------ choice
-// One CTA per (sequence, KV head): the k blocks of the largest keys, ties to the lower
-// index, written in ascending order. Keys are the scores mapped to unsigned integers of the
-// same order; forced blocks get the largest key. The k-th largest key is found bit by bit
-// (32 counts over the CTA), the output places by a prefix sum.
-constexpr int kCThreads = 512, kPer = 8, kCChunk = kCThreads * kPer;
-
+// The k blocks of the largest keys, ties to the lower index, written in ascending order. Keys
+// are the scores mapped to unsigned integers of the same order; forced blocks get the largest
+// key. The k-th largest key is found bit by bit, from the top, until a threshold leaves
+// exactly k keys (or all 32 bits are known and ties are left); the output places come from a
+// prefix sum over the blocks in order.
 __device__ __forceinline__ uint32_t order_key(float x)
 {
     if (x != x) x = -INFINITY;                                 // NaN ranks lowest
@@ -235,113 +375,166 @@ __device__ __forceinline__ uint32_t order_key(float x)
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kCThreads)
-choose_kernel(CacheView c, const float *__restrict__ scores, const uint8_t *__restrict__ modes, int block, int nt, int k,
-              int first, int last, int32_t *__restrict__ ids)
+struct Choice {
+    int nb, k, first, last;
+};
+
+// Sum over WARPS warps (one: no barrier). `slot` alternates between calls.
+template <int WARPS>
+__device__ __forceinline__ int count_all(int n, int (*part)[32], int slot)
 {
-    __shared__ int wsum[2][kCThreads / 32];
-    pdl_wait();
-    pdl_trigger();
-    const int sh = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int nb = (c.len[sh] + block - 1) / block;
-    bool any = !modes;
-    if (modes)
-        for (int g = 0; g < c.G; ++g) any = any || modes[(int64_t)sh * c.G + g] == KVQ_MODE_FULL;
-    int32_t *out = ids + (int64_t)sh * k;
-    const int want = any ? min(k, nb) : 0;
-    for (int i = want + tid; i < k; i += kCThreads) out[i] = -1;
-    if (want == 0) return;
-    const float *sc = scores + (int64_t)sh * nt * kTile;
-    uint32_t key[kPer];
-    auto load = [&](int base) {                                // keys of blocks base + tid * kPer ..; 0 past the end
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (WARPS == 1) return n;
+    if ((threadIdx.x & 31) == 0) part[slot][threadIdx.x >> 5] = n;
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    return __reduce_add_sync(0xffffffffu, lane < WARPS ? part[slot][lane] : 0);
+}
+
+// By WARPS warps (warps 0 .. WARPS - 1 of the block; all threads of the block when more than
+// one), PER keys a thread; more blocks than that are walked in chunks, scores read again.
+template <int WARPS, int PER>
+__device__ __forceinline__ void choose(const float *sc, const Choice &ch, int32_t *__restrict__ out, int (*part)[32])
+{
+    constexpr int T = 32 * WARPS, CH = T * PER;
+    const int tid = threadIdx.x % T, warp = tid >> 5, lane = tid & 31;
+    const int nb = ch.nb, want = min(ch.k, nb);
+    for (int i = want + tid; i < ch.k; i += T) out[i] = -1;
+    uint32_t key[PER];
+    auto load = [&](int base) {                                // keys of blocks base + tid * PER ..; 0 past the end
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int b = base + tid * kPer + e;
+        for (int e = 0; e < PER; ++e) {
+            const int b = base + tid * PER + e;
             key[e] = 0;
-            if (b < nb) key[e] = (b < first || b >= nb - last) ? 0xFFFFFFFFu : order_key(sc[b]);
+            if (b < nb) key[e] = (b < ch.first || b >= nb - ch.last) ? 0xFFFFFFFFu : order_key(sc[b]);
         }
     };
     load(0);
-    uint32_t T = 0;                                            // largest T with at least `want` keys >= T
-    if (want < nb) {
-        for (int bit = 31; bit >= 0; --bit) {
-            const uint32_t t = T | (1u << bit);
-            int n = 0;
-            for (int base = 0; base < nb; base += kCChunk) {
-                if (nb > kCChunk) load(base);
+    // `thr`: the largest threshold known to leave at least `want` keys; `have`: how many it leaves
+    uint32_t thr = 0;
+    int have = nb, slot = 0;
+    for (int bit = 31; bit >= 0 && have != want; --bit) {
+        const uint32_t t = thr | (1u << bit);
+        int n = 0;
+        for (int base = 0; base < nb; base += CH) {
+            if (nb > CH) load(base);
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) n += key[e] >= t ? 1 : 0;
-            }
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0) wsum[bit & 1][warp] = n;
-            __syncthreads();
-            int all = 0;
-#pragma unroll
-            for (int w = 0; w < kCThreads / 32; ++w) all += wsum[bit & 1][w];
-            if (all >= want) T = t;
+            for (int e = 0; e < PER; ++e) n += key[e] >= t ? 1 : 0;
+        }
+        n = count_all<WARPS>(n, part, slot ^= 1);
+        if (n >= want) {
+            thr = t;
+            have = n;
         }
     }
-    __syncthreads();
-    // blocks above T, then those at T in index order until `want` are taken
+    // every key above thr, and those at thr in index order until `want` are taken
     int above = 0;
-    for (int base = 0; base < nb; base += kCChunk) {
-        if (nb > kCChunk) load(base);
+    for (int base = 0; base < nb; base += CH) {
+        if (nb > CH) load(base);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) above += key[e] > T ? 1 : 0;
+        for (int e = 0; e < PER; ++e) above += key[e] > thr ? 1 : 0;
     }
-    above = __reduce_add_sync(0xffffffffu, above);
-    if (lane == 0) wsum[0][warp] = above;
-    __syncthreads();
-    int all = 0;
-    for (int w = 0; w < kCThreads / 32; ++w) all += wsum[0][w];
-    const int ties = want - all;
-    int gt0 = 0, eq0 = 0;                                      // taken so far: above T, at T
-    __syncthreads();
-    for (int base = 0; base < nb; base += kCChunk) {
-        if (nb > kCChunk) load(base);
-        int gt = 0, eq = 0;
+    above = count_all<WARPS>(above, part, slot ^= 1);
+    const int ties = want - above;
+    int gt0 = 0, eq0 = 0;                                      // before this chunk: above thr, at thr
+    for (int base = 0; base < nb; base += CH) {
+        if (nb > CH) load(base);
+        int mine = 0;                                          // above thr | at thr << 16
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const bool in = base + tid * kPer + e < nb;
-            gt += in && key[e] > T ? 1 : 0;
-            eq += in && key[e] == T ? 1 : 0;
+        for (int e = 0; e < PER; ++e) {
+            if (base + tid * PER + e >= nb) break;
+            mine += key[e] > thr ? 1 : key[e] == thr ? 0x10000 : 0;
         }
-        int gi = gt, ei = eq;
+        int upto = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int a = __shfl_up_sync(0xffffffffu, gi, d), b = __shfl_up_sync(0xffffffffu, ei, d);
-            if (lane >= d) {
-                gi += a;
-                ei += b;
-            }
+            const int y = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += y;
         }
-        if (lane == 31) {
-            wsum[0][warp] = gi;
-            wsum[1][warp] = ei;
+        int before = upto - mine, all = __shfl_sync(0xffffffffu, upto, 31);
+        if (WARPS > 1) {
+            __syncthreads();
+            if (lane == 31) part[0][warp] = upto;
+            __syncthreads();
+            const int v = lane < WARPS ? part[0][lane] : 0;
+            before += __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+            all = __reduce_add_sync(0xffffffffu, v);
         }
-        __syncthreads();
-        int gp = gt0 + gi - gt, ep = eq0 + ei - eq, gall = 0, eall = 0;
-        for (int w = 0; w < kCThreads / 32; ++w) {
-            if (w < warp) {
-                gp += wsum[0][w];
-                ep += wsum[1][w];
-            }
-            gall += wsum[0][w];
-            eall += wsum[1][w];
-        }
+        int gp = gt0 + (before & 0xFFFF), ep = eq0 + (before >> 16);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int b = base + tid * kPer + e;
+        for (int e = 0; e < PER; ++e) {
+            const int b = base + tid * PER + e;
             if (b >= nb) break;
-            if (key[e] > T) out[gp++ + min(ep, ties)] = b;
-            else if (key[e] == T) {
+            if (key[e] > thr) out[gp++ + min(ep, ties)] = b;
+            else if (key[e] == thr) {
                 if (ep < ties) out[gp + ep] = b;
                 ++ep;
             }
         }
-        gt0 += gall;
-        eq0 += eall;
-        __syncthreads();
+        gt0 += all & 0xFFFF;
+        eq0 += all >> 16;
+    }
+}
+
+__device__ __forceinline__ void no_blocks(int32_t *out, int k)
+{
+    for (int i = threadIdx.x; i < k; i += blockDim.x) out[i] = -1;
+}
+
+// Scores of one (sequence, KV head, tile) per CTA.
+template <int D, int NQ>
+__global__ void __launch_bounds__(kSThreads)
+score_kernel(CacheView c, const __half *__restrict__ q, const __half *__restrict__ bounds, const uint8_t *__restrict__ modes,
+             int block, int nt, float *__restrict__ scores)
+{
+    __shared__ ScoreSmem<D, NQ> sm;
+    pdl_wait();
+    pdl_trigger();
+    const int sh = blockIdx.x / nt, tile = blockIdx.x % nt;
+    const int nb = (c.len[sh] + block - 1) / block;
+    score_tiles<D, NQ>(c, q, bounds, modes, sh, nb, nt, tile, tile + 1, scores + (int64_t)sh * nt * kTile, nullptr, sm);
+}
+
+// The choice of one (sequence, KV head) per CTA, from scores in memory.
+constexpr int kCPer = 8;
+__global__ void __launch_bounds__(kSThreads)
+choose_kernel(CacheView c, const float *__restrict__ scores, const uint8_t *__restrict__ modes, int block, int nt, int k, int first,
+              int last, int32_t *__restrict__ ids)
+{
+    __shared__ int part[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int sh = blockIdx.x;
+    bool any = !modes;
+    if (modes)
+        for (int g = 0; g < c.G; ++g) any = any || modes[(int64_t)sh * c.G + g] == KVQ_MODE_FULL;
+    const Choice ch{(c.len[sh] + block - 1) / block, k, first, last};
+    if (!any) no_blocks(ids + (int64_t)sh * k, k);
+    else choose<kSWarps, kCPer>(scores + (int64_t)sh * nt * kTile, ch, ids + (int64_t)sh * k, part);
+}
+
+// Both in one launch, a CTA per (sequence, KV head): at most kFuseTiles tiles.
+constexpr int kFuseTiles = 16;
+template <int D, int NQ>
+__global__ void __launch_bounds__(kSThreads)
+select_kernel(CacheView c, const __half *__restrict__ q, const __half *__restrict__ bounds, const uint8_t *__restrict__ modes,
+              int block, int nt, int k, int first, int last, float *__restrict__ scores, int32_t *__restrict__ ids)
+{
+    __shared__ ScoreSmem<D, NQ> sm;
+    __shared__ float keep[kFuseTiles * kTile];
+    __shared__ int part[2][32];
+    pdl_wait();
+    pdl_trigger();
+    const int sh = blockIdx.x;
+    const Choice ch{(c.len[sh] + block - 1) / block, k, first, last};
+    score_tiles<D, NQ>(c, q, bounds, modes, sh, ch.nb, nt, 0, nt, scores + (int64_t)sh * nt * kTile, keep, sm);
+    __syncthreads();
+    int32_t *out = ids + (int64_t)sh * k;
+    if (sm.n_act == 0) no_blocks(out, k);
+    else if (nt > 4) choose<kSWarps, kFuseTiles * kTile / kSThreads>(keep, ch, out, part);
+    else if (threadIdx.x < 32) {
+        if (nt > 2) choose<1, 8>(keep, ch, out, part);
+        else choose<1, 4>(keep, ch, out, part);
     }
 }
 
@@ -356,34 +549,43 @@ cudaError_t launch_block_bounds(const kvq_cache *cache, int block, const int32_t
     const int64_t groups = (nb + kGroup - 1) / kGroup;
     const int per = (int)std::max<int64_t>(1, std::min<int64_t>(groups, (8 * num_sms() + sh - 1) / sh));
     const dim3 grid((unsigned)(sh * per));
-    return c.D == 128 ? launch_pdl(bounds_kernel<128>, grid, dim3(kBThreads), 0, st, c, block, cu, bounds, nt, per)
-                      : launch_pdl(bounds_kernel<64>, grid, dim3(kBThreads), 0, st, c, block, cu, bounds, nt, per);
+    auto launch = [&](auto kernel, size_t smem) {
+        const cudaError_t e = ensure_smem_attr((const void *)kernel, smem);
+        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kBThreads), smem, st, c, block, cu, bounds, nt, per);
+    };
+    if (c.D == 128)
+        return c.ptab ? launch(bounds_kernel<128, true>, sizeof(BoundsSmem<128>))
+                      : launch(bounds_kernel<128, false>, sizeof(BoundsSmem<128>));
+    return c.ptab ? launch(bounds_kernel<64, true>, sizeof(BoundsSmem<64>)) : launch(bounds_kernel<64, false>, sizeof(BoundsSmem<64>));
 }
 
 namespace {
-template <int D>
-cudaError_t launch_scores(const kvq_cache *cache, const __half *q, const __half *bounds, const uint8_t *modes, int block,
-                          int nt, float *scores, cudaStream_t st)
-{
-    const CacheView &c = cache->view;
-    const dim3 grid((unsigned)((int64_t)c.B * c.H * nt));
-    if (c.G == 1) return launch_pdl(score_kernel<D, 1>, grid, dim3(kSThreads), 0, st, c, q, bounds, modes, block, nt, scores);
-    if (c.G == 2) return launch_pdl(score_kernel<D, 2>, grid, dim3(kSThreads), 0, st, c, q, bounds, modes, block, nt, scores);
-    return launch_pdl(score_kernel<D, 4>, grid, dim3(kSThreads), 0, st, c, q, bounds, modes, block, nt, scores);
-}
-} // namespace
-
-cudaError_t launch_select_blocks(const __half *q, const kvq_cache *cache, const __half *bounds, int block,
-                                 const uint8_t *modes, int k, int first, int last, float *scores, int32_t *ids,
-                                 cudaStream_t st)
+template <int D, int NQ>
+cudaError_t launch_select(const __half *q, const kvq_cache *cache, const __half *bounds, int block, const uint8_t *modes, int k,
+                          int first, int last, float *scores, int32_t *ids, cudaStream_t st)
 {
     const CacheView &c = cache->view;
     const int nb = (cache->max_cap + block - 1) / block, nt = (nb + kTile - 1) / kTile;
-    cudaError_t e = c.D == 128 ? launch_scores<128>(cache, q, bounds, modes, block, nt, scores, st)
-                               : launch_scores<64>(cache, q, bounds, modes, block, nt, scores, st);
+    const int64_t sh = (int64_t)c.B * c.H;
+    // one launch when it gives every SM a CTA, or there is a tile only
+    if (nt <= kFuseTiles && (nt == 1 || sh >= num_sms()))
+        return launch_pdl(select_kernel<D, NQ>, dim3((unsigned)sh), dim3(kSThreads), 0, st, c, q, bounds, modes, block, nt, k,
+                          first, last, scores, ids);
+    const cudaError_t e = launch_pdl(score_kernel<D, NQ>, dim3((unsigned)(sh * nt)), dim3(kSThreads), 0, st, c, q, bounds, modes,
+                                     block, nt, scores);
     if (e != cudaSuccess) return e;
-    return launch_pdl(choose_kernel, dim3((unsigned)((int64_t)c.B * c.H)), dim3(kCThreads), 0, st, c,
-                      (const float *)scores, modes, block, nt, k, first, last, ids);
+    return launch_pdl(choose_kernel, dim3((unsigned)sh), dim3(kSThreads), 0, st, c, (const float *)scores, modes, block, nt, k,
+                      first, last, ids);
+}
+} // namespace
+
+cudaError_t launch_select_blocks(const __half *q, const kvq_cache *c, const __half *bounds, int block, const uint8_t *modes,
+                                 int k, int first, int last, float *scores, int32_t *ids, cudaStream_t st)
+{
+    const int G = c->view.G;
+    auto go = [&](auto f) { return f(q, c, bounds, block, modes, k, first, last, scores, ids, st); };
+    if (c->D == 128) return G == 1 ? go(launch_select<128, 1>) : G == 2 ? go(launch_select<128, 2>) : go(launch_select<128, 4>);
+    return G == 1 ? go(launch_select<64, 1>) : G == 2 ? go(launch_select<64, 2>) : go(launch_select<64, 4>);
 }
 
 } // namespace kvq
