@@ -305,6 +305,13 @@ __device__ __forceinline__ void append_seq(const CacheView &c, const __half *__r
             pre[p] = reinterpret_cast<const uint4 *>(row_of(vi & 1, pp / H, pp % H))[li];
         }
     }
+    uint4 preq = make_uint4(0u, 0u, 0u, 0u);     // and of its first query vector
+    if (ROPE && r->q) {
+        const int HQ = H * c.G;
+        const int64_t vi = warp * VPW + lane / VL;
+        if (vi < (int64_t)n * HQ)
+            preq = reinterpret_cast<const uint4 *>(r->q + (t0 + vi / HQ) * r->qs + vi % HQ * D)[li];
+    }
     if (tid == 0) as.bad = 0;
     __syncthreads();
     for (int h = warp; h < H; h += 8) {
@@ -424,8 +431,8 @@ __device__ __forceinline__ void append_seq(const CacheView &c, const __half *__r
             const int hq = (int)(vi % HQ), h = hq / c.G;
             int st = -1;
             if (vi < n_q) st = (h < kAppendHeads) ? as.wstart[h] : c.wstart[s * H + h];
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (st >= 0) x = reinterpret_cast<const uint4 *>(r->q + (t0 + i) * r->qs + (int64_t)hq * D)[li];
+            uint4 x = preq;
+            if (vb >= 8 * VPW && st >= 0) x = reinterpret_cast<const uint4 *>(r->q + (t0 + i) * r->qs + (int64_t)hq * D)[li];
             x = rope_lane<D>(x, st >= 0, r->tab + (st >= 0 ? st + i : 0) * r->rot, *r, li);
             if (st >= 0) reinterpret_cast<uint4 *>(r->q_out + ((t0 + i) * HQ + hq) * D)[li] = x;
         }

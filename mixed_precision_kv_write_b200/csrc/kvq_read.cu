@@ -4,8 +4,9 @@
 // read_kernel: D/8 adjacent lanes per (token, head), 8 channels of K and of V per lane: a lane
 // loads b bytes of each part (2, 4, 8 or 16: its 8 codes) and stores 8 values. A CTA takes
 // kPairs consecutive (token, head) pairs; one thread per pair first finds its sequence
-// (binary search of cu_seqlens), its record offset and its scales. Bound: HBM (records and
-// side entries in, rows out).
+// (binary search of cu_seqlens), its record offset and its scales, then the pairs are sorted
+// by width, so that the lanes of a warp share one code path. Bound: HBM (records and side
+// entries in, rows out).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -16,7 +17,6 @@ namespace kvq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPairs = 64;
 
 struct ReadPair {
     float4 side;
@@ -49,37 +49,38 @@ __device__ __forceinline__ void store8(T *dst, const float (&x)[8])
     }
 }
 
-// the 8 values of chunk li of one record part
-template <int D>
-__device__ __forceinline__ void part_values(const RecLoc &L, int wc, int part, int li, float s, float z, float (&x)[8])
+// chunk li of both parts of one pair
+template <int D, int CLS, typename T>
+__device__ __forceinline__ void pair_values(const ReadPair &pr, uint32_t shift, int li, int64_t at, T *__restrict__ k_out,
+                                            T *__restrict__ v_out)
 {
-    const int b = 2 << wc;
-    const uint8_t *p = L.at((uint32_t)(part * (b * D / 8) + b * li));
-    if (wc == 0) {
-        code_values<0, 8>(make_uint2(*reinterpret_cast<const uint16_t *>(p), 0u), s, z, x);
-    } else if (wc == 1) {
-        code_values<1, 8>(make_uint2(*reinterpret_cast<const uint32_t *>(p), 0u), s, z, x);
-    } else if (wc == 2) {
-        code_values<2, 8>(*reinterpret_cast<const uint2 *>(p), s, z, x);
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        float lo[4], hi[4];
-        code_values<3, 4>(make_uint2(v.x, v.y), s, z, lo);
-        code_values<3, 4>(make_uint2(v.z, v.w), s, z, hi);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            x[e] = lo[e];
-            x[4 + e] = hi[e];
-        }
+    constexpr int BITS = 2 << CLS;
+    RecLoc L;
+    L.base = const_cast<uint8_t *>(pr.base);
+    L.pt = pr.pt;
+    L.off = pr.off;
+    L.shift = shift;
+    const uint4 kw = load_codes<CLS>(L.at(BITS * li)), vw = load_codes<CLS>(L.at(D * BITS / 8 + BITS * li));
+    const float4 sd = pr.side;
+    float x[8];
+    if (k_out) {
+        code_values<CLS>(kw, sd.x, sd.y, x);
+        store8(k_out + at, x);
+    }
+    if (v_out) {
+        code_values<CLS>(vw, sd.z, sd.w, x);
+        store8(v_out + at, x);
     }
 }
 
-template <int D, typename T>
+template <int D, typename T, int kPairs>
 __global__ void __launch_bounds__(kThreads)
 read_kernel(CacheView c, const int32_t *__restrict__ cu, int64_t n_rows, T *__restrict__ k_out, T *__restrict__ v_out)
 {
     constexpr int VL = D / 8;
     __shared__ ReadPair pairs[kPairs];
+    __shared__ uint8_t order[kPairs];
+    __shared__ int cnt[5];                       // pairs by width: end of each width's run, [4] of the rows of zeros
     pdl_wait();
     pdl_trigger();
     const int64_t p0 = (int64_t)blockIdx.x * kPairs;
@@ -124,35 +125,55 @@ read_kernel(CacheView c, const int32_t *__restrict__ cu, int64_t n_rows, T *__re
         pairs[threadIdx.x] = pr;
     }
     __syncthreads();
-    for (int t = threadIdx.x; t < n * VL; t += kThreads) {
-        const int pi = t / VL, li = t % VL;
-        const int wc = pairs[pi].wc;
-        if (wc == -2) continue;
-        float kx[8] = {}, vx[8] = {};
-        if (wc >= 0) {
-            const float4 sd = pairs[pi].side;
-            RecLoc L;
-            L.base = const_cast<uint8_t *>(pairs[pi].base);
-            L.pt = pairs[pi].pt;
-            L.off = pairs[pi].off;
-            L.shift = c.page_shift;
-            if (k_out) part_values<D>(L, wc, 0, li, sd.x, sd.y, kx);
-            if (v_out) part_values<D>(L, wc, 1, li, sd.z, sd.w, vx);
+    if (threadIdx.x < 32) {                      // sort by width; rows left alone are dropped
+        const int lane = threadIdx.x;
+        int base = 0;
+#pragma unroll
+        for (int w = 0; w < 5; ++w) {
+#pragma unroll
+            for (int i = 0; i < kPairs; i += 32) {
+                const bool in = i + lane < n && pairs[i + lane].wc == (w < 4 ? w : -1);
+                const uint32_t m = __ballot_sync(0xffffffffu, in);
+                if (in) order[base + __popc(m & ((1u << lane) - 1u))] = (uint8_t)(i + lane);
+                base += __popc(m);
+            }
+            if (lane == 0) cnt[w] = base;
         }
+    }
+    __syncthreads();
+    const int c0 = cnt[0], c1 = cnt[1], c2 = cnt[2], c3 = cnt[3], c4 = cnt[4];
+    for (int t = threadIdx.x; t < c4 * VL; t += kThreads) {
+        const int oi = t / VL, li = t % VL, pi = order[oi];
         const int64_t at = (p0 + pi) * D + 8 * li;
-        if (k_out) store8(k_out + at, kx);
-        if (v_out) store8(v_out + at, vx);
+        const ReadPair &pr = pairs[pi];
+        if (oi < c0) pair_values<D, 0>(pr, c.page_shift, li, at, k_out, v_out);
+        else if (oi < c1) pair_values<D, 1>(pr, c.page_shift, li, at, k_out, v_out);
+        else if (oi < c2) pair_values<D, 2>(pr, c.page_shift, li, at, k_out, v_out);
+        else if (oi < c3) pair_values<D, 3>(pr, c.page_shift, li, at, k_out, v_out);
+        else {
+            const float zero[8] = {};
+            if (k_out) store8(k_out + at, zero);
+            if (v_out) store8(v_out + at, zero);
+        }
     }
 }
 
-template <typename T>
+template <int D, typename T>
 cudaError_t launch_typed(const kvq_cache *cache, const int32_t *cu, int64_t n_rows, void *k_out, void *v_out,
                          cudaStream_t st)
 {
     const CacheView &c = cache->view;
-    const dim3 grid((unsigned)((n_rows * c.H + kPairs - 1) / kPairs));
-    return c.D == 128 ? launch_pdl(read_kernel<128, T>, grid, dim3(kThreads), 0, st, c, cu, n_rows, (T *)k_out, (T *)v_out)
-                      : launch_pdl(read_kernel<64, T>, grid, dim3(kThreads), 0, st, c, cu, n_rows, (T *)k_out, (T *)v_out);
+    const int64_t n = n_rows * c.H;
+    auto launch = [&](auto kernel, int pairs) {
+        return launch_pdl(kernel, dim3((unsigned)((n + pairs - 1) / pairs)), dim3(kThreads), 0, st, c, cu, n_rows, (T *)k_out,
+                          (T *)v_out);
+    };
+    // 128 pairs a CTA sort better and start fewer CTAs once 8 of them fill every SM (284k pairs:
+    // 43.3 against 45.4 us), 64 spread a short call over more SMs (8k pairs: 6.6 against 9.8 us);
+    // below 32 pairs an SM, one pass of the threads
+    if (n >= (int64_t)128 * 8 * num_sms()) return launch(read_kernel<D, T, 128>, 128);
+    if (n >= (int64_t)32 * num_sms()) return launch(read_kernel<D, T, 64>, 64);
+    return launch(read_kernel<D, T, 16>, 16);
 }
 
 } // namespace
@@ -161,9 +182,10 @@ cudaError_t launch_read(const kvq_cache *c, const int32_t *cu, int64_t n_rows, i
                         cudaStream_t st)
 {
     if (n_rows == 0) return cudaSuccess;
-    if (dtype == KVQ_F32) return launch_typed<float>(c, cu, n_rows, k_out, v_out, st);
-    if (dtype == KVQ_BF16) return launch_typed<__nv_bfloat16>(c, cu, n_rows, k_out, v_out, st);
-    return launch_typed<__half>(c, cu, n_rows, k_out, v_out, st);
+    auto go = [&](auto f128, auto f64) { return (c->D == 128 ? f128 : f64)(c, cu, n_rows, k_out, v_out, st); };
+    if (dtype == KVQ_F32) return go(launch_typed<128, float>, launch_typed<64, float>);
+    if (dtype == KVQ_BF16) return go(launch_typed<128, __nv_bfloat16>, launch_typed<64, __nv_bfloat16>);
+    return go(launch_typed<128, __half>, launch_typed<64, __half>);
 }
 
 } // namespace kvq

@@ -538,14 +538,15 @@ __device__ __forceinline__ void lane_vector(const CacheView &c, const uint4 *vsr
     if (half == 0) reinterpret_cast<float2 *>(&c.side[slot])[part] = make_float2(sc, z);
 }
 
-// The K rows staged in shared memory (pairs of n_pairs (token, head), D values each) rotated in
+// The K rows staged in shared memory (n_pairs (token, head) pairs, D values each) rotated in
 // place, each by its pair's position; refused pairs are left alone. A thread takes a chunk
 // of 8 channels together with its partner chunk, so no value is read after it was changed.
+// Warp 0 sorts the pairs meanwhile, so the others do this.
 template <int D>
 __device__ __forceinline__ void rope_staged(__half *sk, const WqPair *pairs, int n_pairs, const RopeArgs &r)
 {
     const int per = r.interleaved ? r.rot / 8 : r.rot / 16;      // steps per vector
-    for (int t = threadIdx.x; t < n_pairs * per; t += kWqThreads) {
+    for (int t = threadIdx.x - 32; t < n_pairs * per; t += kWqThreads - 32) {
         const int pi = t / per, ci = t % per;
         if (pairs[pi].s < 0) continue;
         const float *row = r.tab + (int64_t)pairs[pi].pos * r.rot;
@@ -562,58 +563,66 @@ __device__ __forceinline__ void rope_staged(__half *sk, const WqPair *pairs, int
     }
 }
 
-// Query rows of kRopeQPairs (token, KV head) pairs from p0 on, rotated into r.q_out; a row
-// whose token was refused stays as it was.
-constexpr int kRopeQPairs = 64;
+// kRopeQVecs query vectors from v0 on, rotated into r.q_out; a row whose token was refused
+// stays as it was. A thread's chunks are loaded before the scan's results are waited for.
+constexpr int kRopeQVecs = 64;
 template <int D>
 __device__ __forceinline__ void rope_q_tile(const CacheView &c, const RopeArgs &r, const int32_t *__restrict__ cu,
-                                            int64_t n_tok, uint32_t gen, int64_t p0, int32_t *pos_sh)
+                                            int64_t n_tok, uint32_t gen, int64_t v0, int32_t *pos_sh)
 {
-    const int H = c.H, G = c.G;
-    const int n = (int)min((int64_t)kRopeQPairs, n_tok * H - p0);
-    pdl_wait();
+    constexpr int STEPS = kRopeQVecs * (D / 8) / kWqThreads;     // steps of a thread, at most
+    const int H = c.H, HQ = H * c.G;
+    const int n = (int)min((int64_t)kRopeQVecs, n_tok * HQ - v0);
+    // a vector's steps: its rotated chunks (half-split: with their partners), then its plain chunks
+    const int rc = r.interleaved ? r.rot / 8 : r.rot / 16;
+    const int per = rc + (D - r.rot) / 8;
+    uint4 x[STEPS], y[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int t = threadIdx.x + i * kWqThreads, vi = t / per, ci = t % per;
+        if (vi < n) {
+            const int64_t tk = (v0 + vi) / HQ;
+            const uint4 *src = reinterpret_cast<const uint4 *>(r.q + tk * r.qs + (int64_t)((v0 + vi) % HQ) * D);
+            x[i] = src[ci < rc ? ci : r.rot / 8 + ci - rc];
+            if (!r.interleaved && ci < rc) y[i] = src[ci + rc];
+        }
+    }
+    int s = 0;
+    const int64_t mine = (v0 + threadIdx.x) / HQ;                // the token of this thread's vector
     if (threadIdx.x < n) {
-        const int64_t tk = (p0 + threadIdx.x) / H;
-        const int h = (int)((p0 + threadIdx.x) % H);
-        int lo = 0, hi = c.B;                    // cu[lo] <= tk < cu[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cu[mid] <= tk) lo = mid;
+        int hi = c.B;                            // cu[s] <= mine < cu[hi]
+        while (hi - s > 1) {
+            const int mid = (s + hi) >> 1;
+            if (cu[mid] <= mine) s = mid;
             else hi = mid;
         }
+    }
+    pdl_wait();
+    if (threadIdx.x < n) {
+        const int h = (int)((v0 + threadIdx.x) % HQ) / c.G;
         int pos = -1;
-        if (tk >= cu[lo] && tk < cu[lo + 1] && c.bad[lo] != gen) {
-            const int st = c.wstart[lo * H + h];
-            if (st >= 0) pos = (int)(st + (tk - cu[lo]));
+        if (mine >= cu[s] && mine < cu[s + 1] && c.bad[s] != gen) {
+            const int st = c.wstart[s * H + h];
+            if (st >= 0) pos = (int)(st + (mine - cu[s]));
         }
         pos_sh[threadIdx.x] = pos;
     }
     __syncthreads();
-    // a vector's steps: its rotated chunks (with their partners), then its plain chunks
-    const int rc = r.interleaved ? r.rot / 8 : r.rot / 16;
-    const int per = rc + (D - r.rot) / 8;
-    for (int t = threadIdx.x; t < n * G * per; t += kWqThreads) {
-        const int vi = t / per, ci = t % per;
-        const int pi = vi / G, g = vi % G;
-        const int pos = pos_sh[pi];
-        if (pos < 0) continue;
-        const int64_t tk = (p0 + pi) / H;
-        const int hq = (int)((p0 + pi) % H) * G + g;
-        const uint4 *src = reinterpret_cast<const uint4 *>(r.q + tk * r.qs + (int64_t)hq * D);
-        uint4 *dst = reinterpret_cast<uint4 *>(r.q_out + (tk * H * G + hq) * D);
-        const float *row = r.tab + (int64_t)pos * r.rot;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const int t = threadIdx.x + i * kWqThreads, vi = t / per, ci = t % per;
+        if (vi >= n || pos_sh[vi] < 0) continue;
+        uint4 *dst = reinterpret_cast<uint4 *>(r.q_out + (v0 + vi) * D);
+        const float *row = r.tab + (int64_t)pos_sh[vi] * r.rot;
         if (ci >= rc) {
-            const int ch = r.rot / 8 + ci - rc;
-            dst[ch] = src[ch];
+            dst[r.rot / 8 + ci - rc] = x[i];
         } else if (r.interleaved) {
-            uint4 x = src[ci];
-            rope_pairs(x, row, 8 * ci, r.rot);
-            dst[ci] = x;
+            rope_pairs(x[i], row, 8 * ci, r.rot);
+            dst[ci] = x[i];
         } else {
-            uint4 x = src[ci], y = src[ci + rc];
-            rope_halves(x, y, row, 8 * ci, r.rot);
-            dst[ci] = x;
-            dst[ci + rc] = y;
+            rope_halves(x[i], y[i], row, 8 * ci, r.rot);
+            dst[ci] = x[i];
+            dst[ci + rc] = y[i];
         }
     }
 }
@@ -644,7 +653,7 @@ __device__ __forceinline__ void write_quant_body(const CacheView &c, const __hal
     const int H = c.H;
     if (ROPE && (int)blockIdx.x >= n_tiles) {
         if (blockIdx.y == 0)
-            rope_q_tile<D>(c, *r, cu, n_tok, gen, (int64_t)((int)blockIdx.x - n_tiles) * kRopeQPairs,
+            rope_q_tile<D>(c, *r, cu, n_tok, gen, (int64_t)((int)blockIdx.x - n_tiles) * kRopeQVecs,
                            reinterpret_cast<int32_t *>(pairs));
         return;
     }
@@ -731,13 +740,12 @@ __device__ __forceinline__ void write_quant_body(const CacheView &c, const __hal
             }
         }
         if (lane == 0) n_written = base;
+    } else if (ROPE) {
+        if (!mbar_wait(&bar, 0, c.status)) return;
+        rope_staged<D>(sk, pairs, Tc * HGc, *r);
     }
     __syncthreads();
     if (!mbar_wait(&bar, 0, c.status)) return;
-    if (ROPE) {
-        rope_staged<D>(sk, pairs, Tc * HGc, *r);
-        __syncthreads();
-    }
 
     // LPV adjacent lanes per vector: vector vi is pair order[vi / 2], K (even) or V (odd);
     // the lanes of a warp take consecutive vectors of the width-sorted list
@@ -860,7 +868,7 @@ cudaError_t launch_write_rope(kvq_cache *cache, const __half *k, const __half *v
     int T, HG;
     quant_tiles(c, n_tok, T, HG);
     const int64_t n_tiles = (n_tok + T - 1) / T;
-    const int64_t q_tiles = r.q ? (n_tok * c.H + kRopeQPairs - 1) / kRopeQPairs : 0;
+    const int64_t q_tiles = r.q ? (n_tok * c.H * c.G + kRopeQVecs - 1) / kRopeQVecs : 0;
     const dim3 grid((unsigned)(n_tiles + q_tiles), (unsigned)((c.H + HG - 1) / HG));
     const size_t smem = 2 * kWqHalves * sizeof(__half);
     le = ensure_smem_attr(c.D == 128 ? (const void *)write_quant_rope_kernel<128>

@@ -285,6 +285,11 @@ def routed_attn_decode_noalloc(q, cache: KVQCache, modes, w: int, out=None, stre
 
 def _rows(t, name, heads, head_dim, device, n=None):
     """Checks fp16 rows [n, heads, head_dim] whose heads are contiguous; returns the row stride."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float16 and t.device == device:
+        shape, st = t.shape, t.stride()
+        if len(shape) == 3 and shape[1] == heads and shape[2] == head_dim and (n is None or shape[0] == n) and \
+                st[2] == 1 and (st[1] == head_dim or heads == 1):
+            return st[0] if shape[0] > 1 else max(st[0], heads * head_dim)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
@@ -293,10 +298,7 @@ def _rows(t, name, heads, head_dim, device, n=None):
         raise TypeError(f"{name} must be {torch.float16} (got {t.dtype})")
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or (n is not None and t.shape[0] != n):
         raise ValueError(f"{name} must have shape {(n, heads, head_dim)} (got {tuple(t.shape)})")
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != head_dim):
-        raise ValueError(f"{name}: the heads of a row must be contiguous (strides {st})")
-    return st[0] if t.shape[0] > 1 else max(st[0], heads * head_dim)
+    raise ValueError(f"{name}: the heads of a row must be contiguous (strides {t.stride()})")
 
 
 def kvq_write_rope(q, k, v, bits, cu_seqlens, cache: KVQCache, cos_sin, interleaved: bool = False, positions=None,
