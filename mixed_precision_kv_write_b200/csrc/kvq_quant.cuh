@@ -153,35 +153,33 @@ struct RopeArgs {
     int rot, interleaved;
 };
 
-__device__ __forceinline__ float rope_lo(float a, float b, float c, float s)
-{
-    return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-}
-__device__ __forceinline__ float rope_hi(float a, float b, float c, float s)
-{
-    return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-}
+// (x.x - y.x, x.y - y.y), each rounded once: -1 times y is exact. A packed sum of packed products
+// would be fused by the compiler (also where both are written as rounding operations), which
+// skips a product's rounding; it leaves this form alone.
+__device__ __forceinline__ float2 sub2_rn(float2 x, float2 y) { return __ffma2_rn(y, make_float2(-1.f, -1.f), x); }
 
-__device__ __forceinline__ void rope_load8(const float *p, float (&f)[8])
+__device__ __forceinline__ void rope_load8(const float *p, float2 (&f)[4])
 {
     const float4 x = __ldg(reinterpret_cast<const float4 *>(p)), y = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-    f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+    f[0] = make_float2(x.x, x.y);
+    f[1] = make_float2(x.z, x.w);
+    f[2] = make_float2(y.x, y.y);
+    f[3] = make_float2(y.z, y.w);
 }
 
 // Channels c .. c + 7 (x) and c + rot/2 .. (y) of one vector, rotated in place; `row` is
 // the position's row of the table, c a multiple of 8 below rot/2.
 __device__ __forceinline__ void rope_halves(uint4 &x, uint4 &y, const float *row, int c, int rot)
 {
-    float cs[8], sn[8];
+    float2 cs[4], sn[4];
     rope_load8(row + c, cs);
     rope_load8(row + rot / 2 + c, sn);
     __half2 *xa = reinterpret_cast<__half2 *>(&x), *yb = reinterpret_cast<__half2 *>(&y);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 a = __half22float2(xa[e]), b = __half22float2(yb[e]);
-        xa[e] = __floats2half2_rn(rope_lo(a.x, b.x, cs[2 * e], sn[2 * e]), rope_lo(a.y, b.y, cs[2 * e + 1], sn[2 * e + 1]));
-        yb[e] = __floats2half2_rn(rope_hi(a.x, b.x, cs[2 * e], sn[2 * e]), rope_hi(a.y, b.y, cs[2 * e + 1], sn[2 * e + 1]));
+        xa[e] = __float22half2_rn(sub2_rn(__fmul2_rn(a, cs[e]), __fmul2_rn(b, sn[e])));
+        yb[e] = __float22half2_rn(sub2_rn(__fmul2_rn(b, cs[e]), __fmul2_rn(a, make_float2(-sn[e].x, -sn[e].y))));
     }
 }
 
@@ -195,7 +193,9 @@ __device__ __forceinline__ void rope_pairs(uint4 &x, const float *row, int c, in
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float2 v = __half22float2(xa[e]);
-        xa[e] = __floats2half2_rn(rope_lo(v.x, v.y, cc[e], ss[e]), rope_hi(v.x, v.y, cc[e], ss[e]));
+        const float2 vc = __fmul2_rn(v, make_float2(cc[e], cc[e]));                    // (a c, b c)
+        const float2 ws = __fmul2_rn(make_float2(v.y, v.x), make_float2(ss[e], -ss[e]));  // (b s, -a s)
+        xa[e] = __float22half2_rn(sub2_rn(vc, ws));
     }
 }
 

@@ -633,7 +633,7 @@ __device__ __forceinline__ void rope_q_tile(const CacheView &c, const RopeArgs &
 // cu_seqlens), the call's verdict, the write start, and the record offset the scan kernel
 // assigned. Then each vector of D values is quantized by one lane from shared memory.
 // ROPE: rows have the strides of `r`; the staged K rows are rotated before they are
-// quantized, and the CTAs from n_tiles on rotate the call's query rows.
+// quantized, and the CTAs beyond the n_tiles rotate the call's query rows.
 template <int D, bool ROPE>
 __device__ __forceinline__ void write_quant_body(const CacheView &c, const __half *__restrict__ k,
                                                  const __half *__restrict__ v, const int32_t *__restrict__ cu,
@@ -651,13 +651,20 @@ __device__ __forceinline__ void write_quant_body(const CacheView &c, const __hal
     // before the first read of what the scan writes (widths verdict, write start, offsets).
     pdl_trigger();
     const int H = c.H;
-    if (ROPE && (int)blockIdx.x >= n_tiles) {
-        if (blockIdx.y == 0)
-            rope_q_tile<D>(c, *r, cu, n_tok, gen, (int64_t)((int)blockIdx.x - n_tiles) * kRopeQVecs,
-                           reinterpret_cast<int32_t *>(pairs));
-        return;
+    uint32_t tile = blockIdx.x;
+    if (ROPE) {
+        // the query tiles are spread evenly among the others: they wait for memory where the
+        // quantization waits for its instructions
+        const uint32_t all = gridDim.x, nq = all - (uint32_t)n_tiles;
+        const uint32_t before = (uint32_t)((uint64_t)blockIdx.x * nq / all);
+        if ((uint32_t)((uint64_t)(blockIdx.x + 1) * nq / all) != before) {
+            if (blockIdx.y == 0)
+                rope_q_tile<D>(c, *r, cu, n_tok, gen, (int64_t)before * kRopeQVecs, reinterpret_cast<int32_t *>(pairs));
+            return;
+        }
+        tile -= before;
     }
-    const int64_t t0 = (int64_t)blockIdx.x * T;
+    const int64_t t0 = (int64_t)tile * T;
     const int h0 = blockIdx.y * HG;
     const int Tc = (int)(n_tok - t0 < T ? n_tok - t0 : T);
     const int HGc = min(HG, H - h0);

@@ -73,6 +73,21 @@ def test_rotates_and_appends(case):
     _same_cache(cache, plain, H, lens)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_every_rounding_of_the_rotation(inter):
+    """Many values, so that a product left unrounded would show (about one row value in 10^5)."""
+    H, D, n = 16, 128, 4096
+    cache = kvq.KVQCache(1, H, D, n)
+    table = rope_table(n, D)
+    q, k, v = _inputs([n], H, 1, D, False, 77)
+    pos = torch.arange(n, device="cuda")
+    got = kvq.kvq_write_rope(q, k, v, torch.full((n, H), 16, dtype=torch.uint8, device="cuda"), cu_of([n]), cache, table,
+                             interleaved=inter)
+    assert torch.equal(got, rotate(q, pos, table, inter))
+    kd, vd = kvq.kvq_read(cache, cu_of([n]), n)
+    assert torch.equal(kd, rotate(k, pos, table, inter)) and torch.equal(vd, v)
+
+
 @pytest.mark.parametrize("n_new", [1, 50])
 def test_positions_roll_back_first(n_new):
     B, H, D = 3, 2, 128
