@@ -563,66 +563,72 @@ __device__ __forceinline__ void rope_staged(__half *sk, const WqPair *pairs, int
     }
 }
 
-// kRopeQVecs query vectors from v0 on, rotated into r.q_out; a row whose token was refused
-// stays as it was. A thread's chunks are loaded before the scan's results are waited for.
-constexpr int kRopeQVecs = 64;
+// A query tile: as many query vectors from v0 on as the staging memory holds, rotated into
+// r.q_out; a row whose token was refused stays as it was. The rows are copied in before the
+// scan's results are waited for.
+template <int D>
+constexpr int kRopeQVecs = 2 * kWqHalves / D;
+
 template <int D>
 __device__ __forceinline__ void rope_q_tile(const CacheView &c, const RopeArgs &r, const int32_t *__restrict__ cu,
-                                            int64_t n_tok, uint32_t gen, int64_t v0, int32_t *pos_sh)
+                                            int64_t n_tok, uint32_t gen, int64_t v0, __half *sq, uint64_t *bar,
+                                            int32_t *pos_sh)
 {
-    constexpr int STEPS = kRopeQVecs * (D / 8) / kWqThreads;     // steps of a thread, at most
     const int H = c.H, HQ = H * c.G;
-    const int n = (int)min((int64_t)kRopeQVecs, n_tok * HQ - v0);
+    const int n = (int)min((int64_t)kRopeQVecs<D>, n_tok * HQ - v0);
+    if (threadIdx.x < 32) {
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * D * 2));
+        __syncwarp();
+        if (r.qs == (int64_t)HQ * D) {
+            if (threadIdx.x == 0) bulk_g2s(sq, r.q + v0 * D, (uint32_t)(n * D * 2), bar);
+        } else {                                                 // a copy per token
+            const int64_t tk0 = v0 / HQ, tk1 = (v0 + n - 1) / HQ;
+            for (int64_t tk = tk0 + threadIdx.x; tk <= tk1; tk += 32) {
+                const int64_t a = max(v0, tk * HQ), e = min(v0 + n, (tk + 1) * HQ);
+                bulk_g2s(sq + (a - v0) * D, r.q + tk * r.qs + (a - tk * HQ) * D, (uint32_t)((e - a) * D * 2), bar);
+            }
+        }
+    }
+    for (int i = threadIdx.x; i < n; i += kWqThreads) {
+        const int64_t tk = (v0 + i) / HQ;
+        int s = 0, hi = c.B;                     // cu[s] <= tk < cu[hi]
+        while (hi - s > 1) {
+            const int mid = (s + hi) >> 1;
+            if (cu[mid] <= tk) s = mid;
+            else hi = mid;
+        }
+        pdl_wait();
+        int pos = -1;
+        if (tk >= cu[s] && tk < cu[s + 1] && c.bad[s] != gen) {
+            const int st = c.wstart[s * H + (int)((v0 + i) % HQ) / c.G];
+            if (st >= 0) pos = (int)(st + (tk - cu[s]));
+        }
+        pos_sh[i] = pos;
+    }
+    pdl_wait();
+    __syncthreads();
+    if (!mbar_wait(bar, 0, c.status)) return;
     // a vector's steps: its rotated chunks (half-split: with their partners), then its plain chunks
     const int rc = r.interleaved ? r.rot / 8 : r.rot / 16;
     const int per = rc + (D - r.rot) / 8;
-    uint4 x[STEPS], y[STEPS];
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int t = threadIdx.x + i * kWqThreads, vi = t / per, ci = t % per;
-        if (vi < n) {
-            const int64_t tk = (v0 + vi) / HQ;
-            const uint4 *src = reinterpret_cast<const uint4 *>(r.q + tk * r.qs + (int64_t)((v0 + vi) % HQ) * D);
-            x[i] = src[ci < rc ? ci : r.rot / 8 + ci - rc];
-            if (!r.interleaved && ci < rc) y[i] = src[ci + rc];
-        }
-    }
-    int s = 0;
-    const int64_t mine = (v0 + threadIdx.x) / HQ;                // the token of this thread's vector
-    if (threadIdx.x < n) {
-        int hi = c.B;                            // cu[s] <= mine < cu[hi]
-        while (hi - s > 1) {
-            const int mid = (s + hi) >> 1;
-            if (cu[mid] <= mine) s = mid;
-            else hi = mid;
-        }
-    }
-    pdl_wait();
-    if (threadIdx.x < n) {
-        const int h = (int)((v0 + threadIdx.x) % HQ) / c.G;
-        int pos = -1;
-        if (mine >= cu[s] && mine < cu[s + 1] && c.bad[s] != gen) {
-            const int st = c.wstart[s * H + h];
-            if (st >= 0) pos = (int)(st + (mine - cu[s]));
-        }
-        pos_sh[threadIdx.x] = pos;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int t = threadIdx.x + i * kWqThreads, vi = t / per, ci = t % per;
-        if (vi >= n || pos_sh[vi] < 0) continue;
+    for (int t = threadIdx.x; t < n * per; t += kWqThreads) {
+        const int vi = t / per, ci = t % per;
+        const int pos = pos_sh[vi];
+        if (pos < 0) continue;
+        const uint4 *src = reinterpret_cast<const uint4 *>(sq + vi * D);
         uint4 *dst = reinterpret_cast<uint4 *>(r.q_out + (v0 + vi) * D);
-        const float *row = r.tab + (int64_t)pos_sh[vi] * r.rot;
+        const float *row = r.tab + (int64_t)pos * r.rot;
         if (ci >= rc) {
-            dst[r.rot / 8 + ci - rc] = x[i];
+            dst[r.rot / 8 + ci - rc] = src[r.rot / 8 + ci - rc];
         } else if (r.interleaved) {
-            rope_pairs(x[i], row, 8 * ci, r.rot);
-            dst[ci] = x[i];
+            uint4 x = src[ci];
+            rope_pairs(x, row, 8 * ci, r.rot);
+            dst[ci] = x;
         } else {
-            rope_halves(x[i], y[i], row, 8 * ci, r.rot);
-            dst[ci] = x[i];
-            dst[ci + rc] = y[i];
+            uint4 x = src[ci], y = src[ci + rc];
+            rope_halves(x, y, row, 8 * ci, r.rot);
+            dst[ci] = x;
+            dst[ci + rc] = y;
         }
     }
 }
@@ -633,7 +639,7 @@ __device__ __forceinline__ void rope_q_tile(const CacheView &c, const RopeArgs &
 // cu_seqlens), the call's verdict, the write start, and the record offset the scan kernel
 // assigned. Then each vector of D values is quantized by one lane from shared memory.
 // ROPE: rows have the strides of `r`; the staged K rows are rotated before they are
-// quantized, and the CTAs beyond the n_tiles rotate the call's query rows.
+// quantized, and the CTAs beyond the n_tiles, which come first, rotate the call's query rows.
 template <int D, bool ROPE>
 __device__ __forceinline__ void write_quant_body(const CacheView &c, const __half *__restrict__ k,
                                                  const __half *__restrict__ v, const int32_t *__restrict__ cu,
@@ -651,19 +657,12 @@ __device__ __forceinline__ void write_quant_body(const CacheView &c, const __hal
     // before the first read of what the scan writes (widths verdict, write start, offsets).
     pdl_trigger();
     const int H = c.H;
-    uint32_t tile = blockIdx.x;
-    if (ROPE) {
-        // the query tiles are spread evenly among the others: they wait for memory where the
-        // quantization waits for its instructions
-        const uint32_t all = gridDim.x, nq = all - (uint32_t)n_tiles;
-        const uint32_t before = (uint32_t)((uint64_t)blockIdx.x * nq / all);
-        if ((uint32_t)((uint64_t)(blockIdx.x + 1) * nq / all) != before) {
-            if (blockIdx.y == 0)
-                rope_q_tile<D>(c, *r, cu, n_tok, gen, (int64_t)before * kRopeQVecs, reinterpret_cast<int32_t *>(pairs));
-            return;
-        }
-        tile -= before;
-    }
+    // The query tiles come first: their copies run while the scan does. (Behind the others they
+    // ran alone at the end, spread among them they took their places: 36 us of a 108 us launch
+    // each way with the rows in registers, 17771 x 16 rows.)
+    const uint32_t nq = ROPE ? gridDim.x - (uint32_t)n_tiles : 0u;
+    if (ROPE && blockIdx.x < nq && blockIdx.y > 0) return;
+    const uint32_t tile = blockIdx.x - nq;
     const int64_t t0 = (int64_t)tile * T;
     const int h0 = blockIdx.y * HG;
     const int Tc = (int)(n_tok - t0 < T ? n_tok - t0 : T);
@@ -677,6 +676,10 @@ __device__ __forceinline__ void write_quant_body(const CacheView &c, const __hal
         fence_mbar_init();
     }
     __syncthreads();
+    if (ROPE && blockIdx.x < nq) {
+        rope_q_tile<D>(c, *r, cu, n_tok, gen, (int64_t)blockIdx.x * kRopeQVecs<D>, sk, &bar, reinterpret_cast<int32_t *>(pairs));
+        return;
+    }
     if (warp == 0) {
         if (lane == 0) mbar_arrive_expect_tx(&bar, 2 * tensor_bytes);
         __syncwarp();
@@ -875,7 +878,8 @@ cudaError_t launch_write_rope(kvq_cache *cache, const __half *k, const __half *v
     int T, HG;
     quant_tiles(c, n_tok, T, HG);
     const int64_t n_tiles = (n_tok + T - 1) / T;
-    const int64_t q_tiles = r.q ? (n_tok * c.H * c.G + kRopeQVecs - 1) / kRopeQVecs : 0;
+    const int64_t q_vecs = c.D == 128 ? kRopeQVecs<128> : kRopeQVecs<64>;
+    const int64_t q_tiles = r.q ? (n_tok * c.H * c.G + q_vecs - 1) / q_vecs : 0;
     const dim3 grid((unsigned)(n_tiles + q_tiles), (unsigned)((c.H + HG - 1) / HG));
     const size_t smem = 2 * kWqHalves * sizeof(__half);
     le = ensure_smem_attr(c.D == 128 ? (const void *)write_quant_rope_kernel<128>
