@@ -10,6 +10,8 @@
 // Layout of the bounds: fp16 [B][H][nt][2][D][64], block n at [n / 64] and [n % 64], 0 = lo
 // and 1 = hi. A channel's bounds of 64 blocks are one 128-byte line, so a query alone on its
 // KV head reads, per channel, only the line that the sign of q_c asks for: half the bytes.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 
 #include "kvq_values.cuh"
@@ -249,7 +251,7 @@ bounds_kernel(CacheView c, int block, const int32_t *__restrict__ cu, __half *__
 // shift and one mask: the fp16 bits moved to the same field of a double (sign, exponent at
 // bit 52 on) are the value times 2^-1008, subnormals included (fp64 arithmetic keeps them).
 // q carries 2^1000, the score 2^8.
-constexpr int kSThreads = 256, kSWarps = kSThreads / 32;
+constexpr int kSThreads = 128, kSWarps = kSThreads / 32;
 constexpr double kQUp = 1.0715086071862673e301;                // 2^1000
 
 __device__ __forceinline__ double half_field(uint32_t top)     // the fp16 bits in bits 16..31 of `top`
@@ -260,7 +262,7 @@ __device__ __forceinline__ double half_field(uint32_t top)     // the fp16 bits 
 // The scores of tiles [t0, t1) of 64 blocks of one (sequence, KV head), by a CTA. Two tiles at a
 // time when there are two (half the warps each), else one. Lane = (channel mod 4, group of 8
 // blocks): a 16-byte load covers 8 blocks of a channel, a warp's load 4 channels. Scores go to
-// `dst`, and to `keep` (shared memory, blocks t0 * 64 on) when given.
+// `dst`, and to `keep` (shared memory) when given.
 template <int D, int NQ>
 struct ScoreSmem {
     double qs[NQ][D];
@@ -312,7 +314,7 @@ __device__ __forceinline__ void score_tiles(const CacheView &c, const __half *__
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[g][e] = 0.0;
             if (some) {
-#pragma unroll 4
+#pragma unroll(NQ == 1 ? 8 : NQ == 2 ? 4 : 2)
                 for (int ch = w0 * 4 + sub; ch < D; ch += 4 * wpt) {
                     uint4 l, u;
                     if (NQ == 1) {
@@ -334,15 +336,21 @@ __device__ __forceinline__ void score_tiles(const CacheView &c, const __half *__
                     }
                 }
             }
+            // over the 4 channels of the lanes that share blocks: halves change hands, so that lane
+            // sub is left with blocks 2 sub, 2 sub + 1 of its 8
 #pragma unroll
-            for (int g = 0; g < NQ; ++g)
+            for (int g = 0; g < NQ; ++g) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    double v = acc[g][e];
-                    v += __shfl_xor_sync(0xffffffffu, v, 8);
-                    v += __shfl_xor_sync(0xffffffffu, v, 16);
-                    if (sub == 0) sm.sum[warp][g][b8 * 8 + e] = v;
+                for (int e = 0; e < 4; ++e) {
+                    const double give = sub & 2 ? acc[g][e] : acc[g][e + 4], have = sub & 2 ? acc[g][e + 4] : acc[g][e];
+                    acc[g][e] = have + __shfl_xor_sync(0xffffffffu, give, 16);
                 }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const double give = sub & 1 ? acc[g][e] : acc[g][e + 2], have = sub & 1 ? acc[g][e + 2] : acc[g][e];
+                    sm.sum[warp][g][b8 * 8 + 2 * sub + e] = have + __shfl_xor_sync(0xffffffffu, give, 8);
+                }
+            }
             __syncthreads();
             if (tid < pair * kTile) {
                 for (int g = 0; g < n; ++g) {
@@ -357,7 +365,7 @@ __device__ __forceinline__ void score_tiles(const CacheView &c, const __half *__
             const int b = t * kTile + tid;
             const float v = b < nb ? best : -INFINITY;
             dst[b] = v;
-            if (keep) keep[b - t0 * kTile] = v;
+            if (keep) keep[b] = v;
         }
     }
 }
@@ -513,25 +521,40 @@ choose_kernel(CacheView c, const float *__restrict__ scores, const uint8_t *__re
     else choose<kSWarps, kCPer>(scores + (int64_t)sh * nt * kTile, ch, ids + (int64_t)sh * k, part);
 }
 
-// Both in one launch, a CTA per (sequence, KV head): at most kFuseTiles tiles.
-constexpr int kFuseTiles = 16;
+// Both in one launch for up to kFuseTiles tiles: a cluster of CTAs per (sequence, KV head), each
+// scoring a run of its tiles; the scores meet in the first one's shared memory, which chooses.
+constexpr int kFuseTiles = 64, kMaxCluster = 8;
 template <int D, int NQ>
 __global__ void __launch_bounds__(kSThreads)
 select_kernel(CacheView c, const __half *__restrict__ q, const __half *__restrict__ bounds, const uint8_t *__restrict__ modes,
-              int block, int nt, int k, int first, int last, float *__restrict__ scores, int32_t *__restrict__ ids)
+              int block, int nt, int k, int first, int last, int n_cta, float *__restrict__ scores, int32_t *__restrict__ ids)
 {
+    namespace cg = cooperative_groups;
     __shared__ ScoreSmem<D, NQ> sm;
-    __shared__ float keep[kFuseTiles * kTile];
     __shared__ int part[2][32];
+    extern __shared__ float keep[];              // nt tiles
     pdl_wait();
     pdl_trigger();
-    const int sh = blockIdx.x;
+    const int sh = blockIdx.x / n_cta, rank = blockIdx.x % n_cta;
     const Choice ch{(c.len[sh] + block - 1) / block, k, first, last};
-    score_tiles<D, NQ>(c, q, bounds, modes, sh, ch.nb, nt, 0, nt, scores + (int64_t)sh * nt * kTile, keep, sm);
-    __syncthreads();
+    const int per = (nt + n_cta - 1) / n_cta, t0 = min(nt, rank * per), t1 = min(nt, t0 + per);
+    float *first_keep = keep;
+    if (n_cta > 1) {
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();                               // the first CTA has started: its shared memory may be written
+        first_keep = cl.map_shared_rank(keep, 0);
+    }
+    score_tiles<D, NQ>(c, q, bounds, modes, sh, ch.nb, nt, t0, t1, scores + (int64_t)sh * nt * kTile, first_keep, sm);
+    if (n_cta > 1) {
+        cg::this_cluster().sync();
+        if (rank > 0) return;
+    } else {
+        __syncthreads();
+    }
     int32_t *out = ids + (int64_t)sh * k;
     if (sm.n_act == 0) no_blocks(out, k);
-    else if (nt > 4) choose<kSWarps, kFuseTiles * kTile / kSThreads>(keep, ch, out, part);
+    else if (nt > 16) choose<kSWarps, kFuseTiles * kTile / kSThreads>(keep, ch, out, part);
+    else if (nt > 4) choose<kSWarps, 16 * kTile / kSThreads>(keep, ch, out, part);
     else if (threadIdx.x < 32) {
         if (nt > 2) choose<1, 8>(keep, ch, out, part);
         else choose<1, 4>(keep, ch, out, part);
@@ -567,10 +590,25 @@ cudaError_t launch_select(const __half *q, const kvq_cache *cache, const __half 
     const CacheView &c = cache->view;
     const int nb = (cache->max_cap + block - 1) / block, nt = (nb + kTile - 1) / kTile;
     const int64_t sh = (int64_t)c.B * c.H;
-    // one launch when it gives every SM a CTA, or there is a tile only
-    if (nt <= kFuseTiles && (nt == 1 || sh >= num_sms()))
-        return launch_pdl(select_kernel<D, NQ>, dim3((unsigned)sh), dim3(kSThreads), 0, st, c, q, bounds, modes, block, nt, k,
-                          first, last, scores, ids);
+    if (nt <= kFuseTiles) {
+        // a CTA per (sequence, KV head), more of them while there are fewer than two an SM
+        const int64_t want = (2 * (int64_t)num_sms() + sh - 1) / sh;
+        const int n_cta = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, kMaxCluster), nt));
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(sh * n_cta));
+        cfg.blockDim = dim3(kSThreads);
+        cfg.dynamicSmemBytes = (size_t)nt * kTile * sizeof(float);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)n_cta;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = n_cta > 1 ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, select_kernel<D, NQ>, c, q, bounds, modes, block, nt, k, first, last, n_cta, scores, ids);
+    }
     const cudaError_t e = launch_pdl(score_kernel<D, NQ>, dim3((unsigned)(sh * nt)), dim3(kSThreads), 0, st, c, q, bounds, modes,
                                      block, nt, scores);
     if (e != cudaSuccess) return e;
