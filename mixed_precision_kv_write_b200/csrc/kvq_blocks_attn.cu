@@ -37,10 +37,6 @@
 // head) and merge at the end; up to 16 CTAs that share one form a cluster and merge through
 // distributed shared memory; more of them leave partial states in the caller's scratch, which
 // a second launch merges.
-//
-// Latency: the records of a tile are asked for as soon as their offsets are known (bulk
-// prefetches into L2, one per 16 consecutive keys), so the loads of the 16-key steps, which
-// each warp issues one step at a time, find them there.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -50,10 +46,8 @@
 namespace kvq {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kQ = 8;                            // query heads per warp
-constexpr int kSteps = 8;                        // 32-key steps of a warp's part of a tile
-constexpr int kTileKeys = kWarps * kSteps * 32;  // keys sorted by width at a time
+constexpr int kTileKeys = 1024;                  // keys a CTA sorts by width at a time
 constexpr int kSlots = kTileKeys + 4 * 16;       // each width's keys are padded to 16
 constexpr float kLazy = 3.f;                     // running-max slack, log2 units
 constexpr float kMInit = -1e30f;                 // running max before the first key
@@ -64,19 +58,17 @@ struct Tile {
     uint2 ent[kSlots];                           // (record offset | kValid | width code, key), sorted
 };
 
-template <int D>
+template <int D, int W>
 struct Smem {
     union {
         Tile tile;
-        float o[kWarps][kQ][D + 4];              // the warps' states: o, then m and l
+        float o[W][kQ][D + 4];              // the warps' states: o, then m and l
     };
     uint4 q[4][D / 32][32];                      // per width: a lane's query operands, 16 bytes at a time
     __half rows[kQ][D + 8];                      // the queries
     float qsum[kQ];
     float done[kQ][D + 4];                       // the CTA's state for the cluster: o, then m and l
-    int cnt[kWarps][4];                          // keys of each width in each warp's part of the tile
-    uint2 some[4];                               // per width: a real key's entry
-    int32_t ids[kTileKeys / 16 + 2];             // the tile's blocks, from the one before its first on
+    int cnt[W][4];                               // keys of each width in each warp's part of the tile
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -180,26 +172,6 @@ __device__ __forceinline__ const uint8_t *byte_at(const RecLoc &L, uint32_t off)
     return PAGED ? L.at(off) : L.base + off;
 }
 
-__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
-// Bytes [o0, o1) of a stream (multiples of 16) into L2, page by page.
-template <bool PAGED>
-__device__ __forceinline__ void prefetch_records(const RecLoc &L, uint32_t o0, uint32_t o1)
-{
-    if constexpr (!PAGED) {
-        prefetch_l2(L.base + o0, o1 - o0);
-    } else {
-        while (o0 < o1) {
-            const uint32_t n = min(o1 - o0, (1u << L.shift) - (o0 & ((1u << L.shift) - 1u)));
-            prefetch_l2(L.at(o0), n);
-            o0 += n;
-        }
-    }
-}
-
 // BYTES bytes of a record at logical offset `off` of the stream (aligned to min(BYTES, 16), so a
 // 16-byte piece lies in one page) into words; 2 bytes fill the low half of one word.
 template <int BYTES, bool PAGED>
@@ -272,11 +244,11 @@ struct KRows {
     }
 };
 
-// Slots base, base + 16 kWarps, .. below `end` of the sorted tile, 16 at a time, all of width
+// Slots base, base + 16 W, .. below `end` of the sorted tile, 16 at a time, all of width
 // 2 << CLS. The next step's K and side entries are loaded while this one's weights are formed
 // (not for native values, whose words take the registers), V while this one's logits are.
-template <int D, int CLS, bool PAGED, int NQ>
-__device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const RecLoc &L, const float4 *side, int base, int end,
+template <int D, int CLS, bool PAGED, int NQ, int W>
+__device__ __forceinline__ void run_class(State<D> &st, const Smem<D, W> &sm, const RecLoc &L, const float4 *side, int base, int end,
                                           bool on0, bool on1)
 {
     const Tile &tl = sm.tile;
@@ -301,7 +273,7 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
     kr.load(tl, L, side, base, g, t);
     if (CLS == 3) set_unit(st, 0x3F800000u);
     else set_unit(st, __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(kr.sa.z, kr.sb.z))));
-    for (int c = base; c < end; c += 16 * kWarps) {
+    for (int c = base; c < end; c += 16 * W) {
         uint32_t v[4][(VB + 3) / 4];
         auto load_v = [&]() {
             const uint4 f0 = *reinterpret_cast<const uint4 *>(&tl.ent[c + 2 * t]);
@@ -347,7 +319,7 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D> &sm, const
         lg[1] = kr.va && on1 ? fmaf(ka, s[1], za * qs1) : -INFINITY;
         lg[2] = kr.vb && on0 ? fmaf(kb, s[2], zb * qs0) : -INFINITY;
         lg[3] = kr.vb && on1 ? fmaf(kb, s[3], zb * qs1) : -INFINITY;
-        if (c + 16 * kWarps < end) kr.load(tl, L, side, c + 16 * kWarps, g, t);
+        if (c + 16 * W < end) kr.load(tl, L, side, c + 16 * W, g, t);
         if (CLS == 3) load_v();
         float mx0 = fmaxf(lg[0], lg[2]), mx1 = fmaxf(lg[1], lg[3]);
         const float smax = fmaxf(sva, svb);
@@ -442,12 +414,13 @@ struct Job {
     float *part;                                 // [unit][n_split][qs][D + 4]
 };
 
-template <int D, bool PAGED, int NQ>
-__global__ void __launch_bounds__(kThreads, 4)
+template <int D, bool PAGED, int NQ, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W)
 decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *__restrict__ out)
 {
+    constexpr int kThreads = 32 * W, kSteps = kTileKeys / kThreads;        // 32-key steps of a warp's part of a tile
     extern __shared__ __align__(16) uint8_t raw[];
-    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw);
+    Smem<D, W> &sm = *reinterpret_cast<Smem<D, W> *>(raw);
     pdl_wait();
     pdl_trigger();
     const int split = blockIdx.x % job.n_split, unit = blockIdx.x / job.n_split;
@@ -498,7 +471,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         sm.q[0][i][ln] = make_uint4(__byte_perm(va.x, vb.x, 0x5410), __byte_perm(va.x, vb.x, 0x7632),
                                     __byte_perm(va.y, vb.y, 0x5410), __byte_perm(va.y, vb.y, 0x7632));
     }
-    for (int qi = warp; qi < kQ; qi += kWarps) {
+    for (int qi = warp; qi < kQ; qi += W) {
         float a = 0.f;
 #pragma unroll
         for (int ch = 0; ch < D; ch += 32) a += __half2float(sm.rows[qi & (NQ - 1)][ch + lane]);
@@ -521,50 +494,44 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
     const RecLoc L = rec_loc(c, s, h, 0);
     const uint32_t *meta = c.meta + slot0;
     const float4 *side = c.side + slot0;
+    const int bs = job.block_shift;
+    const uint32_t below = (1u << lane) - 1u;
     const int a0 = min(e_all, split * share), a1 = min(e_all, a0 + share);
     for (int a = a0; a < a1;) {
         // a tile: up to kTileKeys entries of one kind, the warps' parts multiples of 32
         const bool blocks = a < e_block;
         const int n = min(kTileKeys, (blocks ? min(a1, e_block) : a1) - a);
-        const int per = ((n + kWarps - 1) / kWarps + 31) & ~31;
+        const int per = ((n + W - 1) / W + 31) & ~31;
         const int p0 = warp * per, p1 = min(n, p0 + per);
         const uint32_t act = blocks ? full : local;
-        const int bs = job.block_shift, x0 = (a >> bs) - 1;
-        if (blocks) {
-            for (int i = tid; i < kTileKeys / 16 + 2; i += kThreads) {
-                const int x = x0 + i;
-                sm.ids[i] = x >= 0 && x < job.k ? job.ids[(int64_t)sh * job.k + x] : -1;
+        // lane i < 17: the i-th block of the warp's part, or -1; an entry not above its predecessor
+        // or past the length is dropped
+        const int x0 = (a + p0) >> bs;
+        int id = -1;
+        if (blocks && p0 < p1) {
+            const int x = x0 + lane;
+            const bool in = x <= (a + p1 - 1) >> bs && x < job.k;
+            id = in ? job.ids[(int64_t)sh * job.k + x] : -1;
+            int before = __shfl_up_sync(0xffffffffu, id, 1);
+            if (lane == 0 && x > 0) before = job.ids[(int64_t)sh * job.k + x - 1];
+            if (id >= 0 && (id >= nb || (x > 0 && (before < 0 || id <= before)))) {
+                set_status(c.status, KVQ_ERR_DEVICE_CHECK);
+                id = -1;
             }
         }
-        __syncthreads();
         uint32_t mt[kSteps];
         int js[kSteps];
         int cnt[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-            mt[i] = 0;
-            js[i] = -1;
-            const int e = a + p0 + i * 32 + lane;
+            mt[i] = 0u;
+            js[i] = 0;
             if (p0 + i * 32 >= p1) continue;
-            if (e < a + p1) {
-                if (blocks) {
-                    const int x = e >> bs, id = sm.ids[x - x0], before = sm.ids[x - x0 - 1];
-                    if (id >= 0) {
-                        if ((x > 0 && before < 0) || id <= before || id >= nb) {
-                            set_status(c.status, KVQ_ERR_DEVICE_CHECK);
-                        } else {
-                            const int j = (id << bs) + (e & ((1 << bs) - 1));
-                            if (j < len) js[i] = j;
-                        }
-                    }
-                } else {
-                    js[i] = len - wl + e - e_block;
-                }
-            }
-            if (js[i] >= 0) mt[i] = meta[js[i]] | kValid;
+            const int e = a + p0 + i * 32 + lane;
+            const int b = __shfl_sync(0xffffffffu, id, (e >> bs) - x0);
+            js[i] = blocks ? (b << bs) + (e & ((1 << bs) - 1)) : len - wl + e - e_block;
+            if (e < a + p1 && (!blocks || b >= 0) && js[i] < len) mt[i] = meta[js[i]] | kValid;
         }
-        // 16 consecutive entries are consecutive keys, the valid ones in front: ask for their
-        // side entries and records
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
             if (p0 + i * 32 >= p1) continue;
@@ -574,12 +541,6 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
             cnt[1] += __popc(b0 & ~b1);
             cnt[2] += __popc(b1 & ~b0);
             cnt[3] += __popc(b0 & b1);
-            const int hb = lane & 16, keys = __popc((v >> hb) & 0xFFFFu);
-            const uint32_t last = __shfl_sync(0xffffffffu, mt[i], hb + max(keys - 1, 0));
-            if (lane == hb && keys > 0) {
-                prefetch_l2(side + js[i], 16u * keys);
-                prefetch_records<PAGED>(L, mt[i] & ~15u, (last & ~15u) + ((uint32_t)(D / 2) << (last & 3u)));
-            }
         }
         if (lane < 4) sm.cnt[warp][lane] = lane == 0 ? cnt[0] : lane == 1 ? cnt[1] : lane == 2 ? cnt[2] : cnt[3];
         __syncthreads();
@@ -587,17 +548,17 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         // 4 x + w holds warp x's count of width w; sums over the warps, then over the widths
         int all[4], at[4], first[5];
         {
-            const int mine = lane < 4 * kWarps ? sm.cnt[lane >> 2][lane & 3] : 0;
+            const int mine = lane < 4 * W ? sm.cnt[lane >> 2][lane & 3] : 0;
             int upto = mine;
 #pragma unroll
-            for (int d = 4; d < 4 * kWarps; d <<= 1) {
+            for (int d = 4; d < 4 * W; d <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, upto, d);
                 if (lane >= d) upto += y;
             }
             first[0] = 0;
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                all[w] = __shfl_sync(0xffffffffu, upto, 4 * (kWarps - 1) + w);
+                all[w] = __shfl_sync(0xffffffffu, upto, 4 * (W - 1) + w);
                 at[w] = first[w] + __shfl_sync(0xffffffffu, upto - mine, 4 * warp + w);
                 first[w + 1] = first[w] + ((all[w] + 15) & ~15);
             }
@@ -607,13 +568,16 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
             if (p0 + i * 32 >= p1) continue;
             const uint32_t v = __ballot_sync(0xffffffffu, mt[i] & kValid), b0 = __ballot_sync(0xffffffffu, mt[i] & 1u),
                            b1 = __ballot_sync(0xffffffffu, mt[i] & 2u);
-            const int w = mt[i] & 3;
             if (mt[i] & kValid) {
-                const uint32_t own = v & (w & 1 ? b0 : ~b0) & (w & 2 ? b1 : ~b1);
-                const int to = w & 2 ? (w & 1 ? at[3] : at[2]) : (w & 1 ? at[1] : at[0]);
-                const uint2 ent = make_uint2(mt[i], (uint32_t)js[i]);
-                tl.ent[to + __popc(own & ((1u << lane) - 1u))] = ent;
-                sm.some[w] = ent;                 // any one of them
+                const uint32_t own = v & (mt[i] & 1u ? b0 : ~b0) & (mt[i] & 2u ? b1 : ~b1);
+                const int to = mt[i] & 2u ? (mt[i] & 1u ? at[3] : at[2]) : (mt[i] & 1u ? at[1] : at[0]);
+                const int end = mt[i] & 2u ? (mt[i] & 1u ? first[3] + all[3] : first[2] + all[2])
+                                           : (mt[i] & 1u ? first[1] + all[1] : all[0]);
+                int pos = to + __popc(own & below);
+                tl.ent[pos] = make_uint2(mt[i], (uint32_t)js[i]);
+                // the width's last key also fills its last 16, without kValid
+                if (++pos == end)
+                    for (; pos & 15; ++pos) tl.ent[pos] = make_uint2(mt[i] & ~kValid, (uint32_t)js[i]);
             }
             at[0] += __popc(v & ~b0 & ~b1);
             at[1] += __popc(b0 & ~b1);
@@ -621,24 +585,16 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
             at[3] += __popc(b0 & b1);
         }
         __syncthreads();
-        // padding up to 16: a real record's offset, no kValid
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int to = first[w] + all[w] + lane;
-            if (warp == w && all[w] > 0 && to < first[w + 1])
-                tl.ent[to] = make_uint2(sm.some[w].x & ~kValid, sm.some[w].y);
-        }
-        __syncthreads();
         const bool on0 = (act >> (2 * t & (NQ - 1))) & 1u, on1 = (act >> ((2 * t & (NQ - 1)) + 1)) & 1u;
         // 16-key steps dealt to the warps in turn, so that they run one width's code at a time
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const int b0 = first[w] + ((warp - first[w] / 16) & (kWarps - 1)) * 16, b1 = first[w + 1];
+            const int b0 = first[w] + ((warp - first[w] / 16) & (W - 1)) * 16, b1 = first[w + 1];
             if (b0 >= b1) continue;
-            if (w == 0) run_class<D, 0, PAGED, NQ>(st, sm, L, side, b0, b1, on0, on1);
-            else if (w == 1) run_class<D, 1, PAGED, NQ>(st, sm, L, side, b0, b1, on0, on1);
-            else if (w == 2) run_class<D, 2, PAGED, NQ>(st, sm, L, side, b0, b1, on0, on1);
-            else run_class<D, 3, PAGED, NQ>(st, sm, L, side, b0, b1, on0, on1);
+            if (w == 0) run_class<D, 0, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
+            else if (w == 1) run_class<D, 1, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
+            else if (w == 2) run_class<D, 2, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
+            else run_class<D, 3, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
         }
         a += n;
         __syncthreads();                         // the tile's slots are read; the next one overwrites them
@@ -677,9 +633,9 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
         const int qi = x / D, ch = x % D;
         float M = kMInit, l = 0.f, o = 0.f;
 #pragma unroll
-        for (int wp = 0; wp < kWarps; ++wp) M = fmaxf(M, sm.o[wp][qi][D]);
+        for (int wp = 0; wp < W; ++wp) M = fmaxf(M, sm.o[wp][qi][D]);
 #pragma unroll
-        for (int wp = 0; wp < kWarps; ++wp) {
+        for (int wp = 0; wp < W; ++wp) {
             const float f = ex2(sm.o[wp][qi][D] - M);
             l = fmaf(sm.o[wp][qi][D + 1], f, l);
             o = fmaf(sm.o[wp][qi][ch] + (NQ == 4 ? sm.o[wp][qi + 4][ch] : 0.f), f, o);
@@ -721,14 +677,15 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
 }
 
 // Merges the n_split partial states of each (sequence, query head), a warp per output.
+constexpr int kCombineThreads = 128;
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kCombineThreads)
 decode_blocks_combine_kernel(Job job, int64_t n_out, int G, int nq, float *__restrict__ out)
 {
     constexpr int N = D / 32;
     pdl_wait();
     pdl_trigger();
-    const int64_t hq = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int64_t hq = (int64_t)blockIdx.x * (kCombineThreads / 32) + (threadIdx.x >> 5);
     if (hq >= n_out) return;
     const int lane = threadIdx.x & 31, g = (int)(hq % G);
     const int64_t unit = hq / G * job.n_sub + g / nq;
@@ -761,36 +718,42 @@ int shift_of(int block)
 int queries_per_warp(int G) { return G <= 4 ? 4 : kQ; }
 int subgroups(int G) { return (G + queries_per_warp(G) - 1) / queries_per_warp(G); }
 
-// CTAs per (sequence, KV head, subgroup): enough for a few warps on every SM, at least 64 keys
-// a warp.
-int splits(const kvq_cache *cache, int k, int block, int w)
+// Warps per CTA and CTAs per (sequence, KV head, subgroup). A CTA per unit, of 4 warps, when
+// that gives every SM four of them; else 8 warps, and enough CTAs for two an SM with at least
+// 64 keys a warp. (Batch 64, 16 heads: 62 us with 4 warps, 67 with 8, 74 with 2 CTAs a unit;
+// 20 units of 4096 keys: 17 us with 8 warps, 20.5 with 4.)
+struct Shape {
+    int warps, n_split;
+};
+Shape shape_of(const kvq_cache *cache, int k, int block, int w)
 {
     const CacheView &c = cache->view;
-    const int64_t units = (int64_t)c.B * c.H * (subgroups(c.G));
+    const int64_t units = (int64_t)c.B * c.H * subgroups(c.G), sms = num_sms();
+    if (units >= 4 * sms) return {4, 1};
     const int64_t keys_b = std::min<int64_t>((int64_t)k * block, ((int64_t)cache->max_cap + block - 1) / block * block);
     const int64_t keys_w = std::min<int64_t>((int64_t)w + 1, cache->max_cap);
     const int64_t keys = c.G == 1 ? std::max(keys_b, keys_w) : keys_b + keys_w;
-    const int64_t want = (2 * (int64_t)num_sms() + units - 1) / units;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(want, (keys + 64 * kWarps - 1) / (64 * kWarps)));
+    const int64_t want = (2 * sms + units - 1) / units;
+    return {8, (int)std::max<int64_t>(1, std::min<int64_t>(want, (keys + 64 * 8 - 1) / (64 * 8)))};
 }
 
-template <int D, bool PAGED, int NQ>
+template <int D, bool PAGED, int NQ, int W>
 cudaError_t launch_typed(const kvq_cache *cache, const __half *q, const Job &job, float *out, cudaStream_t st)
 {
     const CacheView &c = cache->view;
-    const size_t smem = sizeof(Smem<D>);
-    cudaError_t e = ensure_smem_attr((const void *)decode_blocks_kernel<D, PAGED, NQ>, smem);
+    const size_t smem = sizeof(Smem<D, W>);
+    cudaError_t e = ensure_smem_attr((const void *)decode_blocks_kernel<D, PAGED, NQ, W>, smem);
     if (e != cudaSuccess) return e;
     const int64_t units = (int64_t)c.B * c.H * job.n_sub;
     const dim3 grid((unsigned)(units * job.n_split));
     if (job.n_split > 8 && job.n_split <= kMaxCluster) {
-        e = ensure_cluster_attr((const void *)decode_blocks_kernel<D, PAGED, NQ>);
+        e = ensure_cluster_attr((const void *)decode_blocks_kernel<D, PAGED, NQ, W>);
         if (e != cudaSuccess) return e;
     }
     if (job.n_split > 1 && job.n_split <= kMaxCluster) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(32 * W);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = st;
         cudaLaunchAttribute attr[2];
@@ -801,23 +764,24 @@ cudaError_t launch_typed(const kvq_cache *cache, const __half *q, const Job &job
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, decode_blocks_kernel<D, PAGED, NQ>, c, q, job, out);
+        return cudaLaunchKernelEx(&cfg, decode_blocks_kernel<D, PAGED, NQ, W>, c, q, job, out);
     }
-    e = launch_pdl(decode_blocks_kernel<D, PAGED, NQ>, grid, dim3(kThreads), smem, st, c, q, job, out);
+    e = launch_pdl(decode_blocks_kernel<D, PAGED, NQ, W>, grid, dim3(32 * W), smem, st, c, q, job, out);
     if (e != cudaSuccess || job.n_split == 1) return e;
     const int64_t n_out = (int64_t)c.B * c.H * c.G;
-    return launch_pdl(decode_blocks_combine_kernel<D>, dim3((unsigned)((n_out + kWarps - 1) / kWarps)), dim3(kThreads), 0, st,
+    return launch_pdl(decode_blocks_combine_kernel<D>, dim3((unsigned)((n_out * 32 + kCombineThreads - 1) / kCombineThreads)),
+                      dim3(kCombineThreads), 0, st,
                       job, n_out, c.G, NQ, out);
 }
 
-template <int NQ>
+template <int NQ, int W>
 cudaError_t launch_nq(const kvq_cache *cache, const __half *q, const Job &job, float *out, cudaStream_t st)
 {
     if (cache->view.ptab)
-        return cache->D == 128 ? launch_typed<128, true, NQ>(cache, q, job, out, st)
-                               : launch_typed<64, true, NQ>(cache, q, job, out, st);
-    return cache->D == 128 ? launch_typed<128, false, NQ>(cache, q, job, out, st)
-                           : launch_typed<64, false, NQ>(cache, q, job, out, st);
+        return cache->D == 128 ? launch_typed<128, true, NQ, W>(cache, q, job, out, st)
+                               : launch_typed<64, true, NQ, W>(cache, q, job, out, st);
+    return cache->D == 128 ? launch_typed<128, false, NQ, W>(cache, q, job, out, st)
+                           : launch_typed<64, false, NQ, W>(cache, q, job, out, st);
 }
 
 } // namespace
@@ -825,7 +789,7 @@ cudaError_t launch_nq(const kvq_cache *cache, const __half *q, const Job &job, f
 int64_t decode_blocks_scratch(const kvq_cache *cache, int k, int block, int w)
 {
     const CacheView &c = cache->view;
-    const int n = splits(cache, k, block, w);
+    const int n = shape_of(cache, k, block, w).n_split;
     if (n <= kMaxCluster) return 0;
     return (int64_t)c.B * c.H * (subgroups(c.G)) * n * std::min(c.G, queries_per_warp(c.G)) * (c.D + 4) * (int64_t)sizeof(float);
 }
@@ -834,18 +798,20 @@ cudaError_t launch_decode_blocks(const __half *q, const kvq_cache *cache, const 
                                  const uint8_t *modes, int w, float *scratch, float *out, cudaStream_t st)
 {
     const CacheView &c = cache->view;
+    const Shape shape = shape_of(cache, k, block, w);
     Job job;
     job.ids = ids;
     job.modes = modes;
     job.k = k;
     job.block_shift = shift_of(block);
     job.w = w;
-    job.n_split = splits(cache, k, block, w);
+    job.n_split = shape.n_split;
     job.n_sub = subgroups(c.G);
     job.qs = std::min(c.G, queries_per_warp(c.G));
     job.part = scratch;
-    if (queries_per_warp(c.G) == 4) return launch_nq<4>(cache, q, job, out, st);
-    return launch_nq<8>(cache, q, job, out, st);
+    if (queries_per_warp(c.G) == 4)
+        return shape.warps == 4 ? launch_nq<4, 4>(cache, q, job, out, st) : launch_nq<4, 8>(cache, q, job, out, st);
+    return shape.warps == 4 ? launch_nq<8, 4>(cache, q, job, out, st) : launch_nq<8, 8>(cache, q, job, out, st);
 }
 
 } // namespace kvq

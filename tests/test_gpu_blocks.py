@@ -100,6 +100,8 @@ def _random_bounds(B, H, nt, D, seed, grid=None):
     ([2000, 800], 1, 9, 128, 16, 40, 2, 0),
     ([70000], 1, 1, 64, 16, 100, 1, 1),                        # more blocks than one pass of the CTA holds
     ([140000, 9], 1, 2, 64, 16, 4096, 3, 5),
+    ([300, 0, 17, 1030] * 25, 3, 1, 128, 16, 9, 1, 1),         # a CTA per (sequence, head)
+    ([5000, 4000] * 50, 3, 2, 64, 64, 20, 0, 1),
 ])
 def test_choice(lens, H, G, D, block, k, first, last):
     cache = kvq.KVQCache(len(lens), H, D, [max(1, L) for L in lens], query_group=G)
@@ -194,6 +196,10 @@ ATTN = [
     ([20000], 1, 1, 128, 128, 157, 20000, 0),
     ([500] * 40, 4, 1, 128, 64, 3, 20, 0),
     ([5000], 2, 20, 128, 32, 130, 257, 4096),
+    # as many (sequence, head)s as start small CTAs, one of them short of a tile, several tiles, or empty
+    ([300, 1, 0, 77] * 20, 8, 1, 128, 64, 5, 33, 0),
+    ([1500, 1100] * 74, 4, 1, 64, 64, 24, 1200, 4096),
+    ([90] * 100, 6, 5, 64, 16, 4, 20, 0),
 ]
 
 

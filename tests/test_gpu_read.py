@@ -36,6 +36,13 @@ def test_rows(dtype, lens, tails, H, D, page):
         assert bool(((got.double() - wide).abs() <= tol).all())
 
 
+def test_many_rows():
+    f = Filled([20000, 1, 900], 8, 64, seed=6)                 # more pairs than start the larger CTAs
+    k, v = kvq.kvq_read(f.cache, f.cu, 20901)
+    f.cache.check()
+    assert torch.equal(k, values32(f.k, f.bits).half()) and torch.equal(v, values32(f.v, f.bits).half())
+
+
 def test_one_output_rows_behind_and_too_many_rows():
     f = Filled([40, 7], 2, 64, seed=3)
     k = torch.full((60, 2, 64), 9.0, device="cuda")
