@@ -503,9 +503,10 @@ score_kernel(CacheView c, const __half *__restrict__ q, const __half *__restrict
     score_tiles<D, NQ>(c, q, bounds, modes, sh, nb, nt, tile, tile + 1, scores + (int64_t)sh * nt * kTile, nullptr, sm);
 }
 
-// The choice of one (sequence, KV head) per CTA, from scores in memory.
-constexpr int kCPer = 8;
-__global__ void __launch_bounds__(kSThreads)
+// The choice of one (sequence, KV head) per CTA, from scores in memory: long contexts, whose
+// scores are read once per bit of the threshold.
+constexpr int kCThreads = 1024, kCPer = 8;
+__global__ void __launch_bounds__(kCThreads)
 choose_kernel(CacheView c, const float *__restrict__ scores, const uint8_t *__restrict__ modes, int block, int nt, int k, int first,
               int last, int32_t *__restrict__ ids)
 {
@@ -518,7 +519,7 @@ choose_kernel(CacheView c, const float *__restrict__ scores, const uint8_t *__re
         for (int g = 0; g < c.G; ++g) any = any || modes[(int64_t)sh * c.G + g] == KVQ_MODE_FULL;
     const Choice ch{(c.len[sh] + block - 1) / block, k, first, last};
     if (!any) no_blocks(ids + (int64_t)sh * k, k);
-    else choose<kSWarps, kCPer>(scores + (int64_t)sh * nt * kTile, ch, ids + (int64_t)sh * k, part);
+    else choose<kCThreads / 32, kCPer>(scores + (int64_t)sh * nt * kTile, ch, ids + (int64_t)sh * k, part);
 }
 
 // Both in one launch for up to kFuseTiles tiles: a cluster of CTAs per (sequence, KV head), each
@@ -612,7 +613,7 @@ cudaError_t launch_select(const __half *q, const kvq_cache *cache, const __half 
     const cudaError_t e = launch_pdl(score_kernel<D, NQ>, dim3((unsigned)(sh * nt)), dim3(kSThreads), 0, st, c, q, bounds, modes,
                                      block, nt, scores);
     if (e != cudaSuccess) return e;
-    return launch_pdl(choose_kernel, dim3((unsigned)sh), dim3(kSThreads), 0, st, c, (const float *)scores, modes, block, nt, k,
+    return launch_pdl(choose_kernel, dim3((unsigned)sh), dim3(kCThreads), 0, st, c, (const float *)scores, modes, block, nt, k,
                       first, last, ids);
 }
 } // namespace

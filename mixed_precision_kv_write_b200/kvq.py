@@ -104,6 +104,13 @@ def _on(device):
     return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
+def _made(stream, *tensors):
+    """Tensors that the call allocated for the current stream, used on `stream` instead."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _check(t, name, dtype, device, shape=None):
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous() and \
             (shape is None or t.shape == shape):
@@ -145,6 +152,7 @@ class KVQCache:
                                               ctypes.cast(arr, ctypes.c_void_p), self.page_bytes,
                                               self.pool_pages, _stream(stream, self.device)))
         self._h = h
+        self._scratch = {}               # bytes of routed_attn_decode_blocks by (k, block, w)
 
     @property
     def handle(self):
@@ -317,6 +325,7 @@ def kvq_write_rope(q, k, v, bits, cu_seqlens, cache: KVQCache, cos_sin, interlea
         qs = _rows(q, "q", cache.query_heads, D, dev, n)
         if q_out is None:
             q_out = torch.empty((n, cache.query_heads, D), dtype=torch.float16, device=dev)
+            _made(stream, q_out)
         _check(q_out, "q_out", torch.float16, dev, (n, cache.query_heads, D))
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -344,8 +353,10 @@ def kvq_read(cache: KVQCache, cu_seqlens, n_rows: int, dtype=torch.float16, k_ou
     shape = (int(n_rows), cache.heads, cache.head_dim)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=dev)
+        _made(stream, k_out)
     if v_out is None:
         v_out = torch.empty(shape, dtype=dtype, device=dev)
+        _made(stream, v_out)
     _check(k_out, "k_out", dtype, dev, shape)
     _check(v_out, "v_out", dtype, dev, shape)
     with _on(dev):
@@ -372,7 +383,8 @@ def block_bounds(cache: KVQCache, block: int, cu_seqlens=None, out=None, stream=
         if out is None:
             raise ValueError("cu_seqlens renews blocks of an `out` that holds the others")
     if out is None:
-        out = torch.zeros(shape, dtype=torch.float16, device=dev)
+        with torch.cuda.stream(stream):                  # (zeroed on the stream that writes it)
+            out = torch.zeros(shape, dtype=torch.float16, device=dev)
     _check(out, "out", torch.float16, dev, shape)
     with _on(dev):
         _raise(load_library().kvq_block_bounds(cache.handle, block, _ptr(cu_seqlens), _ptr(out), _stream(stream, dev)))
@@ -392,8 +404,10 @@ def select_blocks(q, cache: KVQCache, bounds, block: int, k: int, modes=None, fi
         _check(modes, "modes", torch.uint8, dev, (B, cache.query_heads))
     if scores is None:
         scores = torch.empty((B, H, nt * BLOCK_TILE), dtype=torch.float32, device=dev)
+        _made(stream, scores)
     if ids is None:
         ids = torch.empty((B, H, k), dtype=torch.int32, device=dev)
+        _made(stream, ids)
     _check(scores, "scores", torch.float32, dev, (B, H, nt * BLOCK_TILE))
     _check(ids, "ids", torch.int32, dev, (B, H, k))
     with _on(dev):
@@ -414,15 +428,18 @@ def routed_attn_decode_blocks(q, cache: KVQCache, ids, block: int, modes, w: int
         raise ValueError(f"ids must be [{cache.batch}, {cache.heads}, k] (got {tuple(ids.shape)})")
     if out is None:
         out = torch.empty(shape, dtype=torch.float32, device=dev)
+        _made(stream, out)
     _check(out, "out", torch.float32, dev, shape)
-    k, lib = ids.shape[2], load_library()
-    need = lib.routed_attn_decode_blocks_scratch(cache.handle, k, block, int(w))
+    k, w, lib = ids.shape[2], int(w), load_library()
     with _on(dev):
+        need = cache._scratch.get((k, block, w))
+        if need is None:
+            need = cache._scratch[k, block, w] = lib.routed_attn_decode_blocks_scratch(cache.handle, k, block, w)
         scratch = None
         if need > 0:                 # this call's own: allocated for the stream that runs it
             with torch.cuda.stream(stream):
                 scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-        _raise(lib.routed_attn_decode_blocks(_ptr(q), cache.handle, _ptr(ids), k, block, _ptr(modes), int(w),
+        _raise(lib.routed_attn_decode_blocks(_ptr(q), cache.handle, _ptr(ids), k, block, _ptr(modes), w,
                                              _ptr(scratch), max(need, 0), _ptr(out), _stream(stream, dev)))
     return out
 

@@ -125,6 +125,22 @@ def test_choice(lens, H, G, D, block, k, first, last):
         assert torch.equal(ids.cpu(), choose(scores, lens, block, k, first, last))
 
 
+def test_choice_in_a_very_long_context():
+    # one head of 600000 keys, 37500 blocks: several passes of the choosing CTA
+    L, block, k = 600000, 16, 300
+    cache = kvq.KVQCache(1, 1, 64, L)
+    x = torch.zeros((L, 1, 64), dtype=torch.float16, device="cuda")
+    kvq.kvq_write(x, x, torch.full((L, 1), 2, dtype=torch.uint8, device="cuda"), cu_of([L]), cache)
+    bounds = _random_bounds(1, 1, kvq.block_tiles(cache, block), 64, 3, grid=1)
+    q = rows(1, 1, 64, 5).round()                              # many ties
+    ids, scores = kvq.select_blocks(q, cache, bounds, block, k)
+    cache.check()
+    assert torch.equal(ids.cpu(), choose(scores, [L], block, k, 1, 1))
+    out = kvq.routed_attn_decode_blocks(q, cache, ids, block, torch.full((1, 1), 2, dtype=torch.uint8, device="cuda"), 0)
+    cache.check()
+    assert bool((out == 0).all())                              # every value is 0
+
+
 def test_ties_go_to_the_lowest_index_and_order_of_sums_does_not_matter():
     # values on a coarse grid: many equal scores; and channels permuted give the same scores
     lens, H, D, block = [64 * 128], 2, 128, 64
