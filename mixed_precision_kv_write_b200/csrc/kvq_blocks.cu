@@ -29,13 +29,13 @@ constexpr int kTile = KVQ_BLOCK_TILE;    // blocks per tile of the bounds layout
 // for the narrow widths: four cost more in code than they hide). A field at bit p joins the mantissa of m = 2^(23 - p), whose last place there is 1, and
 // one fused multiply-add takes it to fl((m + c) s - m s) = fl(c s), m s being exact. The runs'
 // minima and maxima meet in shared memory as fp16.
-constexpr int kBThreads = 256, kBWarps = kBThreads / 32, kGroup = 16, kMaxSubs = 4, kMaxRun = 64;
+constexpr int kGroup = 16, kMaxSubs = 4, kMaxRun = 64, kRuns = 32;
 
-template <int D>
+template <int D, int W>
 struct BoundsSmem {
     // per run of the group: lo and hi, padded
-    __half part[kMaxSubs * kBWarps][2 * D + 2];
-    uint4 ent[kBWarps][kMaxRun];                               // a run's keys by width: offset, s, z
+    __half part[kRuns][2 * D + 2];
+    uint4 ent[W][kMaxRun];                               // a run's keys by width: offset, s, z
 };
 
 // lo and hi over the n keys of `ent`, all of width 2 << CLS; gk, li: the lane's key of a step and
@@ -104,13 +104,15 @@ __device__ __forceinline__ void bounds_class(__half2 (&lo)[8], __half2 (&hi)[8],
     }
 }
 
-template <int D, bool PAGED>
-__global__ void __launch_bounds__(kBThreads, 4)
+template <int D, bool PAGED, int W>
+__global__ void __launch_bounds__(32 * W, 32 / W)
 bounds_kernel(CacheView c, int block, const int32_t *__restrict__ cu, __half *__restrict__ bounds, int nt, int per_sh)
 {
     constexpr int LPK = D / 16;                                // lanes per key
+    constexpr int kBWarps = W, kBThreads = 32 * W;
+    static_assert(kRuns >= kGroup * (128 / kMaxRun) && kRuns >= (W - 1) * kMaxSubs, "a row per run");
     extern __shared__ __align__(16) uint8_t raw[];
-    BoundsSmem<D> &sm = *reinterpret_cast<BoundsSmem<D> *>(raw);
+    BoundsSmem<D, W> &sm = *reinterpret_cast<BoundsSmem<D, W> *>(raw);
     pdl_wait();
     pdl_trigger();
     const int sh = blockIdx.x / per_sh, s = sh / c.H, h = sh % c.H;
@@ -573,14 +575,22 @@ cudaError_t launch_block_bounds(const kvq_cache *cache, int block, const int32_t
     const int64_t groups = (nb + kGroup - 1) / kGroup;
     const int per = (int)std::max<int64_t>(1, std::min<int64_t>(groups, (8 * num_sms() + sh - 1) / sh));
     const dim3 grid((unsigned)(sh * per));
-    auto launch = [&](auto kernel, size_t smem) {
+    auto launch = [&](auto kernel, size_t smem, int warps) {
         const cudaError_t e = ensure_smem_attr((const void *)kernel, smem);
-        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kBThreads), smem, st, c, block, cu, bounds, nt, per);
+        return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(32 * warps), smem, st, c, block, cu, bounds, nt, per);
     };
-    if (c.D == 128)
-        return c.ptab ? launch(bounds_kernel<128, true>, sizeof(BoundsSmem<128>))
-                      : launch(bounds_kernel<128, false>, sizeof(BoundsSmem<128>));
-    return c.ptab ? launch(bounds_kernel<64, true>, sizeof(BoundsSmem<64>)) : launch(bounds_kernel<64, false>, sizeof(BoundsSmem<64>));
+    // 4 warps a CTA when only new tokens' blocks are renewed (often one: a quarter of it per warp,
+    // and twice as many CTAs in flight: 1024 heads 15.7 -> 13.3 us), 8 when all are
+    if (c.D == 128) {
+        if (cu) return c.ptab ? launch(bounds_kernel<128, true, 4>, sizeof(BoundsSmem<128, 4>), 4)
+                              : launch(bounds_kernel<128, false, 4>, sizeof(BoundsSmem<128, 4>), 4);
+        return c.ptab ? launch(bounds_kernel<128, true, 8>, sizeof(BoundsSmem<128, 8>), 8)
+                      : launch(bounds_kernel<128, false, 8>, sizeof(BoundsSmem<128, 8>), 8);
+    }
+    if (cu) return c.ptab ? launch(bounds_kernel<64, true, 4>, sizeof(BoundsSmem<64, 4>), 4)
+                          : launch(bounds_kernel<64, false, 4>, sizeof(BoundsSmem<64, 4>), 4);
+    return c.ptab ? launch(bounds_kernel<64, true, 8>, sizeof(BoundsSmem<64, 8>), 8)
+                  : launch(bounds_kernel<64, false, 8>, sizeof(BoundsSmem<64, 8>), 8);
 }
 
 namespace {
