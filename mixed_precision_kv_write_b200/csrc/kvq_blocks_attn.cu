@@ -5,14 +5,15 @@
 //
 //   logit_j = q . deq(k_j) / sqrt(D),  p = softmax,  out = sum_j p_j deq(v_j)
 //
-// With codes c, scale s, zero z (Eq. 4), the centred codes c' = c - 2^(b-1) (b < 16) and
-// z' = z + 2^(b-1) s:
-//   q . deq(k_j) = s_j (q . c_j) + z_j sum(q),   sum_j p_j deq(v_j) = sum_j (p_j s_j) c'_j + sum_j p_j z'_j
-// Centring keeps the two sums of V, which run over many keys, from cancelling.
+// With codes c, scale s, zero z (Eq. 4), the centred codes c' = c - (2^b - 1)/2 (b < 16; exact in
+// fp16) and z' = z + (2^b - 1)/2 s:
+//   q . deq(k_j) = s_j (q . c'_j) + z'_j sum(q),   sum_j p_j deq(v_j) = sum_j (p_j s_j) c'_j + sum_j p_j z'_j
+// Centring keeps the sums from cancelling: with K's codes as they are (a mask alone makes a field an
+// fp16 subnormal, two instructions less a pair) the outputs were 9e-6 off, with centred ones 3.5e-7.
 //
 // One warp serves up to 8 query heads of a KV head at once with m16n8k16 matrix
 // instructions (fp16 operands, fp32 sums), 16 keys at a time:
-//   S^T [16 keys x 8 queries]      = C [16 x D] . Q^T [D x 8]            D/16 instructions
+//   S^T [16 keys x 8 queries]      = C' [16 x D] . Q^T [D x 8]           D/16 instructions
 //   O^T [D channels x 8 queries]  += C'^T [D x 16] . W^T [16 x 8]        2 D/16 (up to 4 queries: D/16)
 // The products are exact: q, the codes and native values are fp16 numbers. The weights
 // w = p s are not, so each goes in as two fp16 numbers, w = hi + lo (22 bits), in units that
@@ -25,12 +26,11 @@
 //
 // The keys of a tile (up to 1024 of a CTA's share) are first sorted by width, so that 16 keys
 // of one width unpack by one code path; the warps take the 16-key steps in turn. A 16-bit
-// half of a word holds 16/b codes. For K the two halves are channels of one key (q is stored
-// in the matching order, one order per width) and a mask alone makes an operand: a field in
-// place IS the fp16 subnormal c 2^(pos - 24), and the sums of each position are scaled once
-// per key. For V the halves are the same channels of two keys (one byte permutation), and
-// the fields join the mantissa of 2^(10 - pos), whose last place there is 1, before
-// 2^(10 - pos) + 2^(b-1) is subtracted.
+// half of a word holds 16/b codes: for K the two halves are channels of one key (q is stored
+// in the matching order, one order per width), for V the same channels of two keys (one byte
+// permutation). A field at bit p joins the mantissa of 2^(10 - p), whose last place there is 1,
+// by one mask-and-or, and one addition takes 2^(10 - p) + (2^b - 1)/2 off again. The fields are
+// moved up one place first, so that this constant has its half.
 //
 // Online softmax: the running maximum of a query moves only when a logit exceeds it by
 // more than 3 (log2 units), a warp-uniform branch. The warps of a CTA share a (sequence, KV
@@ -107,61 +107,42 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// The field of BITS bits at SHIFT in both halves of p as fp16 subnormals: c 2^(SHIFT - 24) each.
-template <int BITS, int SHIFT>
-__device__ __forceinline__ uint32_t raw_field(uint32_t p)
-{
-    return p & ((((1u << BITS) - 1u) << SHIFT) * 0x10001u);
-}
-
-// The same field centred, c - 2^(BITS - 1): it joins the mantissa of 2^(10 - SHIFT), whose last
-// place there is 1, then 2^(10 - SHIFT) + 2^(BITS - 1) is subtracted; every step is exact.
+// The fields of BITS bits at SHIFT in both halves of p, centred: c - (2^BITS - 1)/2. A field joins
+// the mantissa of 2^(10 - SHIFT), then 2^(10 - SHIFT) + (2^BITS - 1)/2 is subtracted; every step is
+// exact for SHIFT >= 1.
 template <int BITS, int SHIFT>
 __device__ __forceinline__ uint32_t mid_field(uint32_t p)
 {
     constexpr uint32_t magic = (uint32_t)((25 - SHIFT) << 10) * 0x10001u;
-    constexpr uint32_t off = (0x8000u | (uint32_t)((25 - SHIFT) << 10) | (1u << (BITS - 1 + SHIFT))) * 0x10001u;
-    const uint32_t x = raw_field<BITS, SHIFT>(p) | magic, m = off;
+    constexpr uint32_t off = (0x8000u | (uint32_t)((25 - SHIFT) << 10) | (((1u << BITS) - 1u) << (SHIFT - 1))) * 0x10001u;
+    const uint32_t x = (p & ((((1u << BITS) - 1u) << SHIFT) * 0x10001u)) | magic, m = off;
     const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&m));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // The 16/BITS centred codes in each half of p (LSB-first) as fp16 pairs: x[i] = (field i of
-// the low half, field i of the high half) - 2^(BITS-1).
+// the low half, field i of the high half).
 template <int BITS>
 __device__ __forceinline__ void mid_fields(uint32_t p, uint32_t (&x)[16 / BITS])
 {
-    const uint32_t h = p >> 8;
+    const uint32_t l = p << 1, h = p >> 7;       // the lower and the upper 8 bits, one place up
     if constexpr (BITS == 8) {
-        x[0] = mid_field<8, 0>(p);
-        x[1] = mid_field<8, 0>(h);
+        x[0] = mid_field<8, 1>(l);
+        x[1] = mid_field<8, 1>(h);
     } else if constexpr (BITS == 4) {
-        x[0] = mid_field<4, 0>(p);
-        x[1] = mid_field<4, 4>(p);
-        x[2] = mid_field<4, 0>(h);
-        x[3] = mid_field<4, 4>(h);
+        x[0] = mid_field<4, 1>(l);
+        x[1] = mid_field<4, 5>(l);
+        x[2] = mid_field<4, 1>(h);
+        x[3] = mid_field<4, 5>(h);
     } else {
-        x[0] = mid_field<2, 0>(p);
-        x[1] = mid_field<2, 2>(p);
-        x[2] = mid_field<2, 4>(p);
-        x[3] = mid_field<2, 6>(p);
-        x[4] = mid_field<2, 0>(h);
-        x[5] = mid_field<2, 2>(h);
-        x[6] = mid_field<2, 4>(h);
-        x[7] = mid_field<2, 6>(h);
-    }
-}
-
-// One word of K of two keys (rows g: x, g + 8: y) against its query operands: s[SHIFT / BITS]
-// gains q . c 2^(SHIFT - 24) over the word's fields at SHIFT and SHIFT + 8 of both halves.
-template <int BITS, int SHIFT>
-__device__ __forceinline__ void k_fields(float (&s)[4][4], uint32_t x, uint32_t y, const uint32_t *q)
-{
-    if constexpr (SHIFT < 8) {
-        constexpr int f = SHIFT / BITS;
-        mma(s[f], raw_field<BITS, SHIFT>(x), raw_field<BITS, SHIFT>(y), raw_field<BITS, SHIFT>(x >> 8),
-            raw_field<BITS, SHIFT>(y >> 8), q[f], q[f + 8 / BITS]);
-        k_fields<BITS, SHIFT + BITS>(s, x, y, q);
+        x[0] = mid_field<2, 1>(l);
+        x[1] = mid_field<2, 3>(l);
+        x[2] = mid_field<2, 5>(l);
+        x[3] = mid_field<2, 7>(l);
+        x[4] = mid_field<2, 1>(h);
+        x[5] = mid_field<2, 3>(h);
+        x[6] = mid_field<2, 5>(h);
+        x[7] = mid_field<2, 7>(h);
     }
 }
 
@@ -256,7 +237,7 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D, W> &sm, co
     constexpr int KW = KRows<D, CLS, PAGED>::KW;
     constexpr int VB = D * BITS / 64;            // bytes of a lane's D/8 channels of V
     constexpr int F = 16 / BITS;                 // fields per half word
-    constexpr float mid = (float)(1 << (BITS - 1));
+    constexpr float mid = 0.5f * (float)((1 << BITS) - 1);
     const float cdot = kLog2e / sqrtf((float)D);
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint32_t q[D / 8];
@@ -285,33 +266,33 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D, W> &sm, co
             load_bytes<VB, PAGED>(L, (f1.z & ~15u) + vo, v[3]);
         };
         if (CLS != 3) load_v();
-        // S^T: a word gives 16/BITS operand pairs of its key; equal fields share a sum (for wide codes
-        // two sums alternate), so no chain of dependent instructions is longer than 4
-        float sf[4][4];
+        // S^T: a word gives 16/BITS operand pairs of its key; two sums alternate, so that no chain of
+        // dependent instructions is longer than D/32
+        float sf[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sf[i][0] = sf[i][1] = sf[i][2] = sf[i][3] = 0.f;
+        for (int i = 0; i < 2; ++i) sf[i][0] = sf[i][1] = sf[i][2] = sf[i][3] = 0.f;
         if constexpr (CLS == 3) {
 #pragma unroll
             for (int i = 0; i < KW; i += 2) mma(sf[i / 2 & 1], kr.a[i], kr.b[i], kr.a[i + 1], kr.b[i + 1], q[i], q[i + 1]);
-        } else if constexpr (CLS == 2) {
-#pragma unroll
-            for (int i = 0; i < KW; ++i)
-                mma(sf[i & 1], raw_field<8, 0>(kr.a[i]), raw_field<8, 0>(kr.b[i]), raw_field<8, 0>(kr.a[i] >> 8),
-                    raw_field<8, 0>(kr.b[i] >> 8), q[2 * i], q[2 * i + 1]);
         } else {
 #pragma unroll
-            for (int i = 0; i < KW; ++i) k_fields<BITS, 0>(sf, kr.a[i], kr.b[i], q + i * F);
+            for (int i = 0; i < KW; ++i) {
+                uint32_t xa[F], xb[F];
+                mid_fields<BITS>(kr.a[i], xa);
+                mid_fields<BITS>(kr.b[i], xb);
+#pragma unroll
+                for (int f = 0; f < F; f += 2)
+                    mma(sf[(i * F + f) / 2 & 1], xa[f], xb[f], xa[f + 1], xb[f + 1], q[i * F + f], q[i * F + f + 1]);
+            }
         }
         float s[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (CLS >= 2) s[i] = sf[0][i] + sf[1][i];
-            else if (CLS == 1) s[i] = fmaf(sf[1][i], 0.0625f, sf[0][i]);
-            else s[i] = fmaf(fmaf(fmaf(sf[3][i], 0.25f, sf[2][i]), 0.25f, sf[1][i]), 0.25f, sf[0][i]);
+            s[i] = sf[0][i] + sf[1][i];
         }
         // logits in log2 units: codes entered as c 2^-24
-        const float ka = CLS == 3 ? cdot : kr.sa.x * (cdot * 16777216.f), kb = CLS == 3 ? cdot : kr.sb.x * (cdot * 16777216.f);
-        const float za = CLS == 3 ? 0.f : kr.sa.y, zb = CLS == 3 ? 0.f : kr.sb.y;
+        const float ka = CLS == 3 ? cdot : kr.sa.x * cdot, kb = CLS == 3 ? cdot : kr.sb.x * cdot;
+        const float za = CLS == 3 ? 0.f : fmaf(mid, kr.sa.x, kr.sa.y), zb = CLS == 3 ? 0.f : fmaf(mid, kr.sb.x, kr.sb.y);
         const float sva = CLS == 3 ? 1.f : kr.sa.z, svb = CLS == 3 ? 1.f : kr.sb.z;
         const float zva = CLS == 3 ? 0.f : fmaf(mid, kr.sa.z, kr.sa.w), zvb = CLS == 3 ? 0.f : fmaf(mid, kr.sb.z, kr.sb.w);
         float lg[4];

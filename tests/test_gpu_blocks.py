@@ -251,6 +251,20 @@ def test_attention_one_width_at_a_time(b):
     assert_attention(got, *attention64(f, q, ids, 64, modes, 0), f"b={b}")
 
 
+@pytest.mark.parametrize("G,D", [(1, 128), (2, 64), (4, 128), (8, 128)])
+def test_attention_keeps_single_precision(G, D):
+    """Normal rows, all widths: independent roundings of 2^-24 in the logits (about log2(e) |q||k| /
+    sqrt(D), a few units) and 2^-22 of the weights' exponentials leave a few 1e-7 of the result."""
+    f = Filled([6000] * 3, 2, D, G=G, seed=12)
+    q = rows(3, 2 * G, D, 5)
+    ids = _random_ids(f.lens, 2, 64, 60, 2)
+    ids[:, :, 0] = ids[:, :, 0].clamp(min=0)
+    modes = torch.full((3, 2 * G), 2, dtype=torch.uint8, device="cuda")
+    got = kvq.routed_attn_decode_blocks(q, f.cache, ids, 64, modes, 0).double()
+    ref, _ = attention64(f, q, ids, 64, modes, 0)
+    assert float((got - ref).norm()) <= 1e-6 * float(ref.norm())
+
+
 def test_attention_all_blocks_equals_routed_decode():
     for D, G, page in ((128, 1, 0), (64, 4, 4096)):
         f = Filled([1000, 17, 333], 2, D, G=G, page=page, seed=2)
