@@ -324,7 +324,7 @@ def kvq_write_rope(q, k, v, bits, cu_seqlens, cache: KVQCache, cos_sin, interlea
     if q is not None:
         qs = _rows(q, "q", cache.query_heads, D, dev, n)
         if q_out is None:
-            q_out = torch.empty((n, cache.query_heads, D), dtype=torch.float16, device=dev)
+            q_out = k.new_empty((n, cache.query_heads, D))
             _made(stream, q_out)
         _check(q_out, "q_out", torch.float16, dev, (n, cache.query_heads, D))
     elif q_out is not None:
@@ -352,10 +352,10 @@ def kvq_read(cache: KVQCache, cu_seqlens, n_rows: int, dtype=torch.float16, k_ou
     _check(cu_seqlens, "cu_seqlens", torch.int32, dev, (cache.batch + 1,))
     shape = (int(n_rows), cache.heads, cache.head_dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        k_out = cu_seqlens.new_empty(shape, dtype=dtype)
         _made(stream, k_out)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
+        v_out = cu_seqlens.new_empty(shape, dtype=dtype)
         _made(stream, v_out)
     _check(k_out, "k_out", dtype, dev, shape)
     _check(v_out, "v_out", dtype, dev, shape)
@@ -403,10 +403,10 @@ def select_blocks(q, cache: KVQCache, bounds, block: int, k: int, modes=None, fi
     if modes is not None:
         _check(modes, "modes", torch.uint8, dev, (B, cache.query_heads))
     if scores is None:
-        scores = torch.empty((B, H, nt * BLOCK_TILE), dtype=torch.float32, device=dev)
+        scores = q.new_empty((B, H, nt * BLOCK_TILE), dtype=torch.float32)
         _made(stream, scores)
     if ids is None:
-        ids = torch.empty((B, H, k), dtype=torch.int32, device=dev)
+        ids = q.new_empty((B, H, k), dtype=torch.int32)
         _made(stream, ids)
     _check(scores, "scores", torch.float32, dev, (B, H, nt * BLOCK_TILE))
     _check(ids, "ids", torch.int32, dev, (B, H, k))
@@ -427,7 +427,7 @@ def routed_attn_decode_blocks(q, cache: KVQCache, ids, block: int, modes, w: int
     if ids.dim() != 3 or ids.shape[:2] != (cache.batch, cache.heads):
         raise ValueError(f"ids must be [{cache.batch}, {cache.heads}, k] (got {tuple(ids.shape)})")
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = q.new_empty(shape, dtype=torch.float32)
         _made(stream, out)
     _check(out, "out", torch.float32, dev, shape)
     k, w, lib = ids.shape[2], int(w), load_library()
