@@ -195,13 +195,15 @@ cudaError_t ensure_smem_attr(const void *func, size_t bytes)
 
 cudaError_t ensure_cluster_attr(const void *func)
 {
-    static std::vector<std::pair<const void *, int>> done;
+    // (a full list only means that the attribute is set again)
+    static std::pair<const void *, int> done[64];
+    static int n_done = 0;
     const int dev = current_device();
     std::lock_guard<std::mutex> lock(g_dev_mu);
-    for (const auto &e : done)
-        if (e.first == func && e.second == dev) return cudaSuccess;
+    for (int i = 0; i < n_done; ++i)
+        if (done[i].first == func && done[i].second == dev) return cudaSuccess;
     const cudaError_t err = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (err == cudaSuccess) done.emplace_back(func, dev);
+    if (err == cudaSuccess && n_done < 64) done[n_done++] = {func, dev};
     return err;
 }
 

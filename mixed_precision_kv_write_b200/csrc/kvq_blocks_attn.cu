@@ -65,7 +65,7 @@ template <int D, int W>
 struct Smem {
     union {
         Tile tile;
-        float o[W][kQ][D + 4];              // the warps' states: o, then m and l
+        float o[W][kQ][D + 4];                   // the warps' states: o, then m and l
     };
     uint4 q[4][D / 32][32];                      // per width: a lane's query operands, 16 bytes at a time
     __half rows[kQ][D + 8];                      // the queries
