@@ -9,7 +9,7 @@
 // fp16) and z' = z + (2^b - 1)/2 s:
 //   q . deq(k_j) = s_j (q . c'_j) + z'_j sum(q),   sum_j p_j deq(v_j) = sum_j (p_j s_j) c'_j + sum_j p_j z'_j
 // Centring keeps the sums from cancelling: with K's codes as they are (a mask alone makes a field an
-// fp16 subnormal, two instructions less a pair) the outputs were 9e-6 off, with centred ones 3.5e-7.
+// fp16 subnormal, two instructions less a pair) the outputs were 9e-6 off, with centred ones 3e-7 to 6e-7.
 //
 // One warp serves up to 8 query heads of a KV head at once with m16n8k16 matrix
 // instructions (fp16 operands, fp32 sums), 16 keys at a time:
