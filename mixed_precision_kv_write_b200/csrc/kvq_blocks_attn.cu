@@ -16,10 +16,13 @@
 //   S^T [16 keys x 8 queries]      = C' [16 x D] . Q^T [D x 8]           D/16 instructions
 //   O^T [D channels x 8 queries]  += C'^T [D x 16] . W^T [16 x 8]        2 D/16 (up to 4 queries: D/16)
 // The products are exact: q, the codes and native values are fp16 numbers. The weights
-// w = p s are not, so each goes in as two fp16 numbers, w = hi + lo (22 bits), in units that
-// keep them far from fp16's subnormals: a power of two above the s_V of the keys at hand (1 for
-// native values), times 2^-11 (p is at most 2^3, see below), chosen anew where a width's keys
-// begin and raised where a larger s_V comes. Up to 4 queries leave
+// w = p s are not, so each goes in as two fp16 numbers, w = hi + lo (22 bits), in a unit of the
+// query's own: a power of two that puts the largest w the query has met (relative to its running
+// maximum) at 2^11 to 2^15. A weight is then off by 2^-22 of itself or by 2^-36 of the largest one,
+// whose key moved the sum by half of it or more (no centred code is 0), so keys of large V leave the
+// weights of others alone unless they count. Native values have no scale that bounds them: their
+// weights go in as two tf32 numbers, which have fp32's range, with the values as tf32 (exact), by
+// m16n8k8 instructions, two for one of the others. Up to 4 queries leave
 // columns 4..7 of the instruction to the second numbers. The queries are too few for the
 // 128-row tiles of tcgen05 (G is 1 to 64, and the codes would have to be unpacked to shared
 // memory first).
@@ -52,7 +55,9 @@ namespace {
 constexpr int kQ = 8;                            // query heads per warp
 constexpr int kTileKeys = 1024;                  // keys a CTA sorts by width at a time
 constexpr int kSlots = kTileKeys + 4 * 16;       // each width's keys are padded to 16
-constexpr float kLazy = 3.f;                     // running-max slack, log2 units
+constexpr float kPTop = 8.f;                     // 2^3: the running maximum's slack
+constexpr float kWTop = 32768.f;                 // the largest weight in units of its query
+constexpr int kMaxFac = 64;                      // the smallest unit is 2^-64
 constexpr float kMInit = -1e30f;                 // running max before the first key
 constexpr int kMaxCluster = 16;                  // CTAs of a cluster
 constexpr uint32_t kValid = 4u;                  // meta bit of a real key (bits 0..1: width code)
@@ -87,6 +92,21 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], float a0, float a1, float a2, float a3, float b0, float b1)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+
+__device__ __forceinline__ float to_tf32(float x)              // rounded to tf32's 11 bits
+{
+    uint32_t y;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(y) : "f"(x));
+    return __uint_as_float(y);
 }
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)     // an 8x8 matrix of 16-bit values
@@ -183,28 +203,44 @@ __device__ __forceinline__ void load_bytes(const RecLoc &L, uint32_t off, uint32
 
 // A warp's attention state. Lane (g, t) = (lane / 4, lane % 4): m, l, pz of queries 2t, 2t + 1
 // (l and pz over the lane's own keys), o[mt] = channels g D/8 + 2 mt (entries 0, 1) and + 1
-// (entries 2, 3) of those queries, in units of `unit`.
+// (entries 2, 3) of those queries, times fac (a power of two, 1 / unit).
 template <int D>
 struct State {
     float o[D / 16][4];
-    float m[2], l[2], pz[2];
-    float unit;
+    float m[2], l[2], pz[2], fac[2];
 };
 
-// The state's unit becomes S / 2^11, S the power of two above the scale whose bits are `top`.
-template <int D>
-__device__ __forceinline__ void set_unit(State<D> &st, uint32_t top)
+// The running maxima take in the logits lg of the step's keys (entries 0, 1 of the key with scale
+// sva, 2, 3 of the one with svb), the units their weights. A unit only grows relative to 2^m, so
+// the sums shrink; the largest weight at hand comes to 2^11 to 2^12 units.
+template <int D, int CLS>
+__device__ __forceinline__ void raise(State<D> &st, const float (&lg)[4], float sva, float svb)
 {
-    const int e = min(max((int)(top >> 23) + 1, 87), 167);      // biased exponent of S
-    const float unit = __uint_as_float((uint32_t)(e - 11) << 23), r = st.unit / unit;   // exact
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-        st.o[i][0] *= r;
-        st.o[i][1] *= r;
-        st.o[i][2] *= r;
-        st.o[i][3] *= r;
+    for (int j = 0; j < 2; ++j) {
+        float n = fmaxf(lg[j], lg[2 + j]);
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, d));
+        n = fmaxf(st.m[j], n);
+        const int have = (int)(__float_as_uint(st.fac[j]) >> 23) - 127;
+        int f = min(kMaxFac, have + (int)fminf(n - st.m[j], 256.f));
+        if (CLS != 3) {
+            float w = fmaxf(ex2(lg[j] - n) * sva, ex2(lg[2 + j] - n) * svb);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, d));
+            f = min(f, 12 + 126 - (int)(__float_as_uint(w) >> 23));            // w < 2^(exponent bits - 126)
+        }
+        const float c = ex2(st.m[j] - n), r = ex2(st.m[j] - n + (float)(f - have));
+        st.m[j] = n;
+        st.l[j] *= c;
+        st.pz[j] *= c;
+        st.fac[j] = __uint_as_float((uint32_t)(f + 127) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            st.o[i][j] *= r;
+            st.o[i][2 + j] *= r;
+        }
     }
-    st.unit = unit;
 }
 
 // K's words and the side entries of a 16-key step's rows g and g + 8.
@@ -255,8 +291,6 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D, W> &sm, co
     const float qs0 = sm.qsum[2 * t] * cdot, qs1 = sm.qsum[2 * t + 1] * cdot;
     KRows<D, CLS, PAGED> kr;
     kr.load(tl, L, side, base, g, t);
-    if (CLS == 3) set_unit(st, 0x3F800000u);
-    else set_unit(st, __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(kr.sa.z, kr.sb.z))));
     for (int c = base; c < end; c += 16 * W) {
         uint32_t v[4][(VB + 3) / 4];
         auto load_v = [&]() {
@@ -293,7 +327,7 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D, W> &sm, co
         for (int i = 0; i < 4; ++i) {
             s[i] = sf[0][i] + sf[1][i];
         }
-        // logits in log2 units: codes entered as c 2^-24
+        // logits in log2 units: (s (q . c') + z' sum(q)) log2(e) / sqrt(D)
         const float ka = CLS == 3 ? cdot : kr.sa.x * cdot, kb = CLS == 3 ? cdot : kr.sb.x * cdot;
         const float za = CLS == 3 ? 0.f : fmaf(mid, kr.sa.x, kr.sa.y), zb = CLS == 3 ? 0.f : fmaf(mid, kr.sb.x, kr.sb.y);
         const float sva = CLS == 3 ? 1.f : kr.sa.z, svb = CLS == 3 ? 1.f : kr.sb.z;
@@ -305,52 +339,59 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D, W> &sm, co
         lg[3] = kr.vb && on1 ? fmaf(kb, s[3], zb * qs1) : -INFINITY;
         if (c + 16 * W < end) kr.load(tl, L, side, c + 16 * W, g, t);
         if (CLS == 3) load_v();
-        float mx0 = fmaxf(lg[0], lg[2]), mx1 = fmaxf(lg[1], lg[3]);
-        const float smax = fmaxf(sva, svb);
-        // (the unit is raised before a scale reaches S = 2^11 units)
-        if (__any_sync(0xffffffffu, mx0 > st.m[0] + kLazy || mx1 > st.m[1] + kLazy || (CLS != 3 && smax > 2048.f * st.unit))) {
+        float p[4], w[4];
+        auto weights = [&]() {
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, d));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, d));
-            }
-            const float n0 = fmaxf(st.m[0], mx0), n1 = fmaxf(st.m[1], mx1);
-            const float c0 = ex2(st.m[0] - n0), c1 = ex2(st.m[1] - n1);
-            st.m[0] = n0;
-            st.m[1] = n1;
-            st.l[0] *= c0;
-            st.l[1] *= c1;
-            st.pz[0] *= c0;
-            st.pz[1] *= c1;
+            for (int i = 0; i < 4; ++i) p[i] = ex2(lg[i] - st.m[i & 1]);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                st.o[i][0] *= c0;
-                st.o[i][1] *= c1;
-                st.o[i][2] *= c0;
-                st.o[i][3] *= c1;
-            }
-            if (CLS != 3) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(smax));
-                if (__uint_as_float(top) > 2048.f * st.unit) set_unit(st, top);
-            }
+            for (int i = 0; i < 4; ++i) w[i] = p[i] * (CLS == 3 ? st.fac[i & 1] : (i < 2 ? sva : svb) * st.fac[i & 1]);
+        };
+        weights();
+        bool over = fmaxf(p[0], p[2]) > kPTop || fmaxf(p[1], p[3]) > kPTop;
+        if (CLS != 3) over = over || fmaxf(w[0], w[2]) > kWTop || fmaxf(w[1], w[3]) > kWTop;
+        if (__any_sync(0xffffffffu, over)) {
+            raise<D, CLS>(st, lg, sva, svb);
+            weights();
         }
-        float p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = ex2(lg[i] - st.m[i & 1]);
         st.l[0] += p[0] + p[2];
         st.l[1] += p[1] + p[3];
         if (CLS != 3) {
             st.pz[0] = fmaf(p[0], zva, fmaf(p[2], zvb, st.pz[0]));
             st.pz[1] = fmaf(p[1], zva, fmaf(p[3], zvb, st.pz[1]));
         }
-        const float fac = __uint_as_float((254u << 23) - __float_as_uint(st.unit));    // 1 / unit, a power of two
-        const float w0 = CLS == 3 ? fac : sva * fac, w1 = CLS == 3 ? fac : svb * fac;
-        p[0] *= w0;
-        p[1] *= w0;
-        p[2] *= w1;
-        p[3] *= w1;
-        uint32_t h0 = pack_half(p[0], p[1]), h1 = pack_half(p[2], p[3]);
-        const uint32_t r0 = rest_half(p[0], p[1], h0), r1 = rest_half(p[2], p[3], h1);
+        if constexpr (CLS == 3) {
+            // the fp32 weights transposed as two 16-bit halves: x[i] is that of key 2t, 2t + 1, 8 + 2t,
+            // 9 + 2t and the lane's query g
+            float x[4], y[4];
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const uint32_t w0 = __float_as_uint(w[i]), w1 = __float_as_uint(w[i + 1]);
+                const uint32_t up = transpose8(__byte_perm(w0, w1, 0x7632)), low = transpose8(__byte_perm(w0, w1, 0x5410));
+                x[i] = __uint_as_float(__byte_perm(low, up, 0x5410));
+                x[i + 1] = __uint_as_float(__byte_perm(low, up, 0x7632));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float h = to_tf32(x[i]);
+                y[i] = x[i] - h;
+                x[i] = NQ == 4 && g >= 4 ? y[i] : h;                // columns 4..7 carry the rests of queries 0..3
+            }
+            // rows g and g + 8 of the instruction are a word's two channels
+#pragma unroll
+            for (int i = 0; i < VB / 4; ++i) {
+                const float2 f0 = h2_values(v[0][i]), f1 = h2_values(v[1][i]);
+                const float2 f2 = h2_values(v[2][i]), f3 = h2_values(v[3][i]);
+                mma_tf32(st.o[i], f0.x, f0.y, f1.x, f1.y, x[0], x[1]);
+                mma_tf32(st.o[i], f2.x, f2.y, f3.x, f3.y, x[2], x[3]);
+                if (NQ == 8) {
+                    mma_tf32(st.o[i], f0.x, f0.y, f1.x, f1.y, y[0], y[1]);
+                    mma_tf32(st.o[i], f2.x, f2.y, f3.x, f3.y, y[2], y[3]);
+                }
+            }
+            continue;
+        }
+        const uint32_t h0 = pack_half(w[0], w[1]), h1 = pack_half(w[2], w[3]);
+        const uint32_t r0 = rest_half(w[0], w[1], h0), r1 = rest_half(w[2], w[3], h1);
         uint32_t bh0, bh1, bl0 = 0u, bl1 = 0u;
         if (NQ == 4) {                           // columns 4..7 carry the rests of queries 0..3
             bh0 = transpose8(t < 2 ? h0 : r0);
@@ -368,14 +409,7 @@ __device__ __forceinline__ void run_class(State<D> &st, const Smem<D, W> &sm, co
             for (int half = 0; half < (VB >= 4 ? 2 : 1); ++half) {
                 const uint32_t sel = half ? 0x7632 : 0x5410;
                 const uint32_t pa = __byte_perm(v[0][i], v[1][i], sel), pb = __byte_perm(v[2][i], v[3][i], sel);
-                if constexpr (F == 1) {
-                    // one channel per half: rows g and g + 8 of the instruction are the word's two halves
-                    if (half == 0) {
-                        const uint32_t qa = __byte_perm(v[0][i], v[1][i], 0x7632), qb = __byte_perm(v[2][i], v[3][i], 0x7632);
-                        mma(st.o[i], pa, qa, pb, qb, bh0, bh1);
-                        if (NQ == 8) mma(st.o[i], pa, qa, pb, qb, bl0, bl1);
-                    }
-                } else {
+                if constexpr (CLS != 3) {
                     uint32_t xa[F], xb[F];
                     mid_fields<BITS>(pa, xa);
                     mid_fields<BITS>(pb, xb);
@@ -472,8 +506,8 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
     for (int i = 0; i < 2; ++i) {
         st.m[i] = kMInit;
         st.l[i] = st.pz[i] = 0.f;
+        st.fac[i] = 1.f;
     }
-    st.unit = 1.f;
     Tile &tl = sm.tile;
     const RecLoc L = rec_loc(c, s, h, 0);
     const uint32_t *meta = c.meta + slot0;
@@ -600,11 +634,11 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float *o = sm.o[warp][2 * t + i];
-            const float add = rest ? 0.f : st.pz[i];
+            const float add = rest ? 0.f : st.pz[i], unit = __uint_as_float((254u << 23) - __float_as_uint(st.fac[i]));
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt)
                 *reinterpret_cast<float2 *>(&o[g * (D / 8) + 2 * mt]) =
-                    make_float2(fmaf(st.o[mt][i], st.unit, add), fmaf(st.o[mt][2 + i], st.unit, add));
+                    make_float2(fmaf(st.o[mt][i], unit, add), fmaf(st.o[mt][2 + i], unit, add));
             if (g == 0 && !rest) {
                 o[D] = st.m[i];
                 o[D + 1] = st.l[i];
