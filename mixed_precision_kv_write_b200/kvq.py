@@ -104,11 +104,17 @@ def _on(device):
     return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
-def _made(stream, *tensors):
-    """Tensors that the call allocated for the current stream, used on `stream` instead."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _result(stream, like, shape, dtype):
+    """A tensor of the call's own, next to `like`. When the call runs on another stream, the memory is
+    taken while that one is current: what it held before was last used there, so the call does not
+    overwrite a tensor that work pending on the caller's stream still reads. The caller goes on
+    with it on the current stream, so it is not handed out again before that has passed."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with torch.cuda.stream(stream):
+        t = like.new_empty(shape, dtype=dtype)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
 
 
 def _check(t, name, dtype, device, shape=None):
@@ -324,8 +330,7 @@ def kvq_write_rope(q, k, v, bits, cu_seqlens, cache: KVQCache, cos_sin, interlea
     if q is not None:
         qs = _rows(q, "q", cache.query_heads, D, dev, n)
         if q_out is None:
-            q_out = k.new_empty((n, cache.query_heads, D))
-            _made(stream, q_out)
+            q_out = _result(stream, k, (n, cache.query_heads, D), torch.float16)
         _check(q_out, "q_out", torch.float16, dev, (n, cache.query_heads, D))
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -352,11 +357,9 @@ def kvq_read(cache: KVQCache, cu_seqlens, n_rows: int, dtype=torch.float16, k_ou
     _check(cu_seqlens, "cu_seqlens", torch.int32, dev, (cache.batch + 1,))
     shape = (int(n_rows), cache.heads, cache.head_dim)
     if k_out is None:
-        k_out = cu_seqlens.new_empty(shape, dtype=dtype)
-        _made(stream, k_out)
+        k_out = _result(stream, cu_seqlens, shape, dtype)
     if v_out is None:
-        v_out = cu_seqlens.new_empty(shape, dtype=dtype)
-        _made(stream, v_out)
+        v_out = _result(stream, cu_seqlens, shape, dtype)
     _check(k_out, "k_out", dtype, dev, shape)
     _check(v_out, "v_out", dtype, dev, shape)
     with _on(dev):
@@ -385,6 +388,8 @@ def block_bounds(cache: KVQCache, block: int, cu_seqlens=None, out=None, stream=
     if out is None:
         with torch.cuda.stream(stream):                  # (zeroed on the stream that writes it)
             out = torch.zeros(shape, dtype=torch.float16, device=dev)
+        if stream is not None:                           # (and the caller goes on with it on the current one)
+            out.record_stream(torch.cuda.current_stream(dev))
     _check(out, "out", torch.float16, dev, shape)
     with _on(dev):
         _raise(load_library().kvq_block_bounds(cache.handle, block, _ptr(cu_seqlens), _ptr(out), _stream(stream, dev)))
@@ -403,11 +408,9 @@ def select_blocks(q, cache: KVQCache, bounds, block: int, k: int, modes=None, fi
     if modes is not None:
         _check(modes, "modes", torch.uint8, dev, (B, cache.query_heads))
     if scores is None:
-        scores = q.new_empty((B, H, nt * BLOCK_TILE), dtype=torch.float32)
-        _made(stream, scores)
+        scores = _result(stream, q, (B, H, nt * BLOCK_TILE), torch.float32)
     if ids is None:
-        ids = q.new_empty((B, H, k), dtype=torch.int32)
-        _made(stream, ids)
+        ids = _result(stream, q, (B, H, k), torch.int32)
     _check(scores, "scores", torch.float32, dev, (B, H, nt * BLOCK_TILE))
     _check(ids, "ids", torch.int32, dev, (B, H, k))
     with _on(dev):
@@ -427,8 +430,7 @@ def routed_attn_decode_blocks(q, cache: KVQCache, ids, block: int, modes, w: int
     if ids.dim() != 3 or ids.shape[:2] != (cache.batch, cache.heads):
         raise ValueError(f"ids must be [{cache.batch}, {cache.heads}, k] (got {tuple(ids.shape)})")
     if out is None:
-        out = q.new_empty(shape, dtype=torch.float32)
-        _made(stream, out)
+        out = _result(stream, q, shape, torch.float32)
     _check(out, "out", torch.float32, dev, shape)
     k, w, lib = ids.shape[2], int(w), load_library()
     with _on(dev):
