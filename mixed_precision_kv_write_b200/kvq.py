@@ -105,15 +105,17 @@ def _on(device):
 
 
 def _result(stream, like, shape, dtype):
-    """A tensor of the call's own, next to `like`. When the call runs on another stream, the memory is
-    taken while that one is current: what it held before was last used there, so the call does not
-    overwrite a tensor that work pending on the caller's stream still reads. The caller goes on
-    with it on the current stream, so it is not handed out again before that has passed."""
+    """A tensor of the call's own, next to the tensor `like` or on that device. When the call runs on
+    another stream, the memory is taken while that one is current: what it held before was last
+    used there, so the call does not overwrite a tensor that work pending on the caller's stream
+    still reads. The caller goes on with it on the current stream, so it is not handed out again
+    before that has passed."""
     if stream is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(shape, dtype=dtype) if isinstance(like, torch.Tensor) else \
+            torch.empty(shape, dtype=dtype, device=like)
     with torch.cuda.stream(stream):
-        t = like.new_empty(shape, dtype=dtype)
-    t.record_stream(torch.cuda.current_stream(like.device))
+        t = _result(None, like, shape, dtype)
+    t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 
@@ -184,7 +186,7 @@ class KVQCache:
         _raise(load_library().kvq_cache_truncate(self._h, _ptr(lengths), _stream(stream, self.device)))
 
     def lengths(self, stream=None) -> torch.Tensor:
-        out = torch.empty(self.batch, dtype=torch.int32, device=self.device)
+        out = _result(stream, self.device, (self.batch,), torch.int32)
         _raise(load_library().kvq_cache_lengths(self._h, _ptr(out), _stream(stream, self.device)))
         return out
 
@@ -195,10 +197,10 @@ class KVQCache:
     def export(self, seq: int, head: int, first: int, count: int, stream=None):
         """(k_codes uint16 [count, D], v_codes, side fp32 [count, 4], bits uint8 [count])."""
         D = self.head_dim
-        kc = torch.empty((count, D), dtype=torch.int16, device=self.device)
-        vc = torch.empty((count, D), dtype=torch.int16, device=self.device)
-        sd = torch.empty((count, 4), dtype=torch.float32, device=self.device)
-        bt = torch.empty((count,), dtype=torch.uint8, device=self.device)
+        kc = _result(stream, self.device, (count, D), torch.int16)
+        vc = _result(stream, self.device, (count, D), torch.int16)
+        sd = _result(stream, self.device, (count, 4), torch.float32)
+        bt = _result(stream, self.device, (count,), torch.uint8)
         _raise(load_library().kvq_cache_export(self._h, seq, head, first, count, _ptr(kc), _ptr(vc),
                                                _ptr(sd), _ptr(bt), _stream(stream, self.device)))
         return kc, vc, sd, bt
@@ -234,7 +236,7 @@ def routed_attn_prefill(q, cache: KVQCache, modes, w: int, cu_seqlens, out=None,
     _check(modes, "modes", torch.uint8, dev, (n, cache.query_heads))
     _check(cu_seqlens, "cu_seqlens", torch.int32, dev, (cache.batch + 1,))
     if out is None:
-        out = torch.empty((n, cache.query_heads, cache.head_dim), dtype=torch.float32, device=dev)
+        out = _result(stream, q, (n, cache.query_heads, cache.head_dim), torch.float32)
     _check(out, "out", torch.float32, dev, (n, cache.query_heads, cache.head_dim))
     _raise(load_library().routed_attn_prefill(_ptr(q), cache.handle, _ptr(modes), int(w),
                                               _ptr(cu_seqlens), n, _ptr(out), _stream(stream, dev)))
@@ -248,7 +250,7 @@ def routed_attn_decode(q, cache: KVQCache, modes, w: int, out=None, stream=None)
     _check(q, "q", torch.float16, dev, shape)
     _check(modes, "modes", torch.uint8, dev, shape[:2])
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = _result(stream, q, shape, torch.float32)
     _check(out, "out", torch.float32, dev, shape)
     _raise(load_library().routed_attn_decode(_ptr(q), cache.handle, _ptr(modes), int(w), _ptr(out),
                                              _stream(stream, dev)))
@@ -272,7 +274,7 @@ def decode_step(q, k, v, bits, cu_seqlens, cache: KVQCache, modes, w: int, posit
     if positions is not None:
         _check(positions, "positions", torch.int32, dev, (cache.batch,))
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = _result(stream, q, shape, torch.float32)
     _check(out, "out", torch.float32, dev, shape)
     _raise(load_library().kvq_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(bits), _ptr(cu_seqlens), n,
                                           _ptr(positions), _ptr(modes), int(w), cache.handle, _ptr(out),
@@ -290,7 +292,7 @@ def routed_attn_decode_noalloc(q, cache: KVQCache, modes, w: int, out=None, stre
     _check(q, "q", torch.float16, dev, shape)
     _check(modes, "modes", torch.uint8, dev, shape[:2])
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = _result(stream, q, shape, torch.float32)
     _check(out, "out", torch.float32, dev, shape)
     _raise(load_library().routed_attn_decode_noalloc(_ptr(q), cache.handle, _ptr(modes), int(w),
                                                      _ptr(out), _stream(stream, dev)))
@@ -466,7 +468,7 @@ def route_argmax(z_attn=None, z_bits=None, stream=None):
         if n is not None and rows != n:
             raise ValueError("route_argmax: z_attn and z_bits have different row counts")
         n = rows
-        outs.append(torch.empty(z.shape[:-1], dtype=torch.uint8, device=dev))
+        outs.append(_result(stream, z, z.shape[:-1], torch.uint8))
     _raise(load_library().kvq_route_argmax(_ptr(z_attn) if z_attn is not None else None,
                                            _ptr(z_bits) if z_bits is not None else None, n,
                                            _ptr(outs[0]) if outs[0] is not None else None,

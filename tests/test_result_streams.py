@@ -63,22 +63,35 @@ def watch(monkeypatch):
     return w
 
 
+class _OnGpu(torch.Tensor):
+    """route_argmax takes logits on a GPU alone."""
+    device = types.SimpleNamespace(type="cuda", index=0)
+
+
 B, H, G, D, BLOCK = 2, 2, 2, 64, 16
 
 
 def _calls():
     cache = types.SimpleNamespace(device=torch.device("cpu"), batch=B, heads=H, head_dim=D, query_group=G, query_heads=H * G,
-                                  capacity=[40] * B, handle=None, _scratch={})
+                                  capacity=[40] * B, handle=None, _h=None, _scratch={})
     q, kv = torch.zeros((B, H * G, D), dtype=torch.float16), torch.zeros((B, H, D), dtype=torch.float16)
     bits, cu = torch.full((B, H), 4, dtype=torch.uint8), torch.tensor([0, 1, 2], dtype=torch.int32)
     modes = torch.full((B, H * G), 2, dtype=torch.uint8)
     bounds = torch.zeros((B, H, 1, 2, D, 64), dtype=torch.float16)
     ids, table = torch.zeros((B, H, 3), dtype=torch.int32), torch.zeros((40, D))
+    logits = torch.zeros((B, H, 3)).as_subclass(_OnGpu)
     return {
         "kvq_write_rope": lambda **s: kvq.kvq_write_rope(q, kv, kv, bits, cu, cache, table, **s),
         "kvq_read": lambda **s: kvq.kvq_read(cache, cu, 2, **s),
         "block_bounds": lambda **s: kvq.block_bounds(cache, BLOCK, **s),
         "select_blocks": lambda **s: kvq.select_blocks(q, cache, bounds, BLOCK, 3, modes, **s),
+        "routed_attn_prefill": lambda **s: kvq.routed_attn_prefill(q, cache, modes, 4, cu, **s),
+        "routed_attn_decode": lambda **s: kvq.routed_attn_decode(q, cache, modes, 4, **s),
+        "routed_attn_decode_noalloc": lambda **s: kvq.routed_attn_decode_noalloc(q, cache, modes, 4, **s),
+        "decode_step": lambda **s: kvq.decode_step(q, kv, kv, bits, cu, cache, modes, 4, **s),
+        "lengths": lambda **s: kvq.KVQCache.lengths(cache, **s),
+        "export": lambda **s: kvq.KVQCache.export(cache, 0, 0, 0, 1, **s),
+        "route_argmax": lambda **s: kvq.route_argmax(logits, None, **s),
         "routed_attn_decode_blocks": lambda **s: kvq.routed_attn_decode_blocks(q, cache, ids, BLOCK, modes, 4, **s),
     }
 
@@ -88,7 +101,7 @@ def test_results_belong_to_the_stream_of_the_call(name, watch):
     call = _calls()[name]
     with watch:
         results = call(stream=SIDE)
-    results = results if isinstance(results, tuple) else (results,)
+    results = [r for r in (results if isinstance(results, tuple) else (results,)) if r is not None]
     assert watch.lib.streams == [SIDE.cuda_stream]
     assert watch.made and all(stream is SIDE for _, stream in watch.made)
     for r in results:
