@@ -266,8 +266,12 @@ int kvq_read(const kvq_cache *cache, const int32_t *cu_seqlens, int64_t n_rows, 
  * to fp16 (no counterpart in the paper: the index that kvq_select_blocks reads).
  *   cu_seqlens: NULL: every block that holds a key. Else int32 [batch + 1]: only the blocks that
  *               hold one of the last cu_seqlens[s+1] - cu_seqlens[s] tokens of sequence s (each
- *               from its first key on): call it with a write's cu_seqlens after the write, and the
- *               bounds stay those of the whole cache, roll-backs by kvq_cache_truncate included.
+ *               from its first key on), and of a sequence without new tokens its last block when
+ *               that is not full, which a roll-back may have cut. Call it with a write's cu_seqlens
+ *               after the write, and the bounds are again those of the whole cache, whatever the write
+ *               or kvq_cache_truncate rolled back before. (Between a roll-back and this call the cut
+ *               block keeps the bounds of the dropped keys.) More tokens than the sequence holds:
+ *               all its blocks (KVQ_ERR_DEVICE_CHECK).
  *   bounds:     fp16 [batch][heads][nt][2][head_dim][64], 16-byte aligned, owned by the
  *               caller; nt = ceil(ceil(max capacity / block) / 64). Block n of a head is at
  *               [n / 64][..][..][n % 64]; [0] minima, [1] maxima. Other entries are left as

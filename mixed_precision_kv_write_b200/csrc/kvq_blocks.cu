@@ -123,10 +123,11 @@ bounds_kernel(CacheView c, int block, const int32_t *__restrict__ cu, __half *__
         const int64_t n = (int64_t)cu[s + 1] - cu[s];
         if (n < 0 || n > len) {
             if (threadIdx.x == 0 && blockIdx.x % per_sh == 0) set_status(c.status, KVQ_ERR_DEVICE_CHECK);
-            return;
+            if (n < 0) return;
         }
-        if (n == 0) return;
-        first = len - (int)n;
+        // without new tokens, the last block may have been cut by a roll-back (at its border it was whole)
+        if (n == 0 && len % block == 0) return;
+        first = max(0, len - (int)max(n, (int64_t)1));
     }
     const int b_lo = first / block, b_hi = (len + block - 1) / block;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, li = lane % LPK, gk = lane / LPK;

@@ -1,0 +1,61 @@
+"""Calls of the rotating write and of block-sparse decoding at the edges of what their contracts
+allow: sequences without new tokens, roll-backs, empty and refused writes."""
+import pytest
+import torch
+
+from blocks_testlib import Filled, cu_of, flat_bounds, rope_table, rows, widths
+from mixed_precision_kv_write_b200 import kvq
+
+pytestmark = pytest.mark.gpu
+
+
+def _same_bounds(cache, bounds, block, lens):
+    fresh = flat_bounds(kvq.block_bounds(cache, block))
+    for s, L in enumerate(lens):
+        nb = -(-L // block)
+        assert torch.equal(flat_bounds(bounds)[s, ..., :nb], fresh[s, ..., :nb]), s
+
+
+# ------------------------------------------------------------------ bounds
+@pytest.mark.parametrize("block,page", [(16, 0), (64, 4096), (128, 0)])
+@pytest.mark.parametrize("by", ["truncate", "positions"])
+def test_bounds_of_a_sequence_rolled_back_without_new_tokens(block, page, by):
+    lens, D = [400, 300, 131, 128, 5], 64
+    f = Filled(lens, 2, D, page=page, seed=9, capacity=[500] * 5)
+    f.k[20:40] *= 20                                           # (extremes that a cut may drop)
+    table = rope_table(500, D)
+    bounds = kvq.block_bounds(f.cache, block)
+    for i, (back, new) in enumerate([([395, 300, 130, 3, 4], [0, 2, 0, 0, 0]), ([1, 256, 128, 0, -1], [0, 0, 0, 0, 1]),
+                                     ([0, 255, 127, -1, 2], [0, 0, 0, 3, 0])]):
+        pos, n = torch.tensor(back, dtype=torch.int32, device="cuda"), sum(new)
+        k, v, bits = rows(n, 2, D, i), rows(n, 2, D, i + 5), widths(n, 2, i)
+        if by == "truncate":
+            f.cache.truncate(pos)
+            kvq.kvq_write(k, v, bits, cu_of(new), f.cache)
+        else:
+            kvq.kvq_write_rope(None, k, v, bits, cu_of(new), f.cache, table, positions=pos)
+        lens = [(min(L, b) if b >= 0 else L) + m for L, b, m in zip(lens, back, new)]
+        kvq.block_bounds(f.cache, block, cu_of(new), out=bounds)
+        f.cache.check()
+        assert f.cache.lengths().tolist() == lens
+        _same_bounds(f.cache, bounds, block, lens)
+
+
+def test_bounds_after_a_refused_write():
+    """A roll-back stands although the write behind it is refused: the bounds follow."""
+    D, block = 64, 32
+    f = Filled([100, 40], 2, D, seed=2, capacity=[120, 60])
+    bounds = kvq.block_bounds(f.cache, block)
+    n = 130
+    pos = torch.tensor([50, 33], dtype=torch.int32, device="cuda")
+    kvq.kvq_write_rope(None, rows(n, 2, D, 1), rows(n, 2, D, 2), widths(n, 2, 3), cu_of([90, 40]), f.cache, rope_table(500, D),
+                       positions=pos)
+    with pytest.raises(kvq.KVQError) as e:
+        f.cache.check()
+    assert e.value.code == kvq.KVQ_ERR_CAPACITY
+    kvq.block_bounds(f.cache, block, cu_of([90, 40]), out=bounds)
+    with pytest.raises(kvq.KVQError) as e:
+        f.cache.check()
+    assert e.value.code == kvq.KVQ_ERR_DEVICE_CHECK
+    assert f.cache.lengths().tolist() == [50, 33]
+    _same_bounds(f.cache, bounds, block, [50, 33])
