@@ -28,7 +28,8 @@ namespace {
 // and assigns the new tokens' record offsets with a parallel prefix sum of the record
 // sizes b*D/4. The new length/end are committed by the quantize kernel, which sees the
 // per-sequence verdict of every head. max_len: no sequence may grow past it (the rows of
-// the position table of a rotating write; INT32_MAX otherwise).
+// the position table of a rotating write; INT32_MAX otherwise); one without new tokens may be
+// longer.
 template <int TPS, int BS = (TPS < 256 ? 256 : TPS)>
 __global__ void __launch_bounds__(BS)
 write_scan_kernel(CacheView c, const uint8_t *__restrict__ bits, const int32_t *__restrict__ cu,
@@ -56,7 +57,7 @@ write_scan_kernel(CacheView c, const uint8_t *__restrict__ bits, const int32_t *
     }
     const int n = (int)(t1 - t0);
     const int L0 = c.len[sh];
-    if ((int64_t)L0 + n > min(c.cap[s], max_len)) {
+    if (n > 0 && (int64_t)L0 + n > min(c.cap[s], max_len)) {
         if (tid == 0) {
             set_status(c.status, KVQ_ERR_CAPACITY);
             c.wstart[sh] = -1;
@@ -187,7 +188,7 @@ write_scan_chunk_kernel(CacheView c, const uint8_t *__restrict__ bits, const int
     }
     const int n = (int)(t1 - t0);
     if (ck > 0 && ck * kScanChunk >= n) return;  // past this sequence's tokens
-    if ((int64_t)L0 + n > cap) {
+    if (n > 0 && (int64_t)L0 + n > cap) {
         if (ck == 0 && tid == 0) {
             set_status(c.status, KVQ_ERR_CAPACITY);
             c.wstart[sh] = -1;

@@ -59,3 +59,23 @@ def test_bounds_after_a_refused_write():
     assert e.value.code == kvq.KVQ_ERR_DEVICE_CHECK
     assert f.cache.lengths().tolist() == [50, 33]
     _same_bounds(f.cache, bounds, block, [50, 33])
+
+
+# ------------------------------------------------------------------ rotating write
+@pytest.mark.parametrize("n_new", [1, 30, 400])                # one launch; both forms of the scan
+def test_a_sequence_without_new_tokens_may_be_longer_than_the_table(n_new):
+    B, H, D = 3, 2, 64
+    lens = [500, 20, 0]
+    f = Filled(lens, H, D, seed=4, capacity=[600, 600, 600])
+    counts = [0, n_new, 1]
+    n = sum(counts)
+    kvq.kvq_write_rope(None, rows(n, H, D, 1), rows(n, H, D, 2), widths(n, H, 3), cu_of(counts), f.cache,
+                       rope_table(20 + n_new, D))
+    f.cache.check()                                            # nothing was refused
+    assert f.cache.lengths().tolist() == [500, 20 + n_new, 1]
+    kvq.kvq_write_rope(None, rows(n, H, D, 1), rows(n, H, D, 2), widths(n, H, 3), cu_of(counts), f.cache,
+                       rope_table(20 + n_new, D))              # sequence 1 would pass the table's end now
+    with pytest.raises(kvq.KVQError) as e:
+        f.cache.check()
+    assert e.value.code == kvq.KVQ_ERR_CAPACITY
+    assert f.cache.lengths().tolist() == [500, 20 + n_new, 2]
