@@ -510,13 +510,13 @@ int kvq_write_rope(const void *q, int64_t q_stride, const void *k, int64_t k_str
         return fail(KVQ_ERR_ARG, "kvq_write_rope: a row stride is below the row's size or not a multiple of 8");
     if (!on_device(c)) return fail(KVQ_ERR_ARG, "kvq_write_rope: the cache's device is not the current device");
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (!kvq::write_is_short(c, n_tok)) {
+    if (n_tok > 0 && !kvq::write_is_short(c, n_tok)) {
         // a long write's kernels recognise their own call's marks by the call's number, which a
-        // replayed graph would repeat
+        // replayed graph would repeat (without tokens, only the roll-back is launched)
         cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
         if (cudaStreamIsCapturing(st, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) {
             cudaGetLastError();
-            return fail(KVQ_ERR_ARG, "kvq_write_rope: only writes of at most 2 * batch tokens can be captured");
+            return fail(KVQ_ERR_ARG, "kvq_write_rope: only writes of at most 2 * batch (and 4096) tokens can be captured");
         }
     }
     kvq::RopeArgs r;

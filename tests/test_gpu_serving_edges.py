@@ -79,3 +79,25 @@ def test_a_sequence_without_new_tokens_may_be_longer_than_the_table(n_new):
         f.cache.check()
     assert e.value.code == kvq.KVQ_ERR_CAPACITY
     assert f.cache.lengths().tolist() == [500, 20 + n_new, 2]
+
+
+def test_an_empty_write_is_captured():
+    """No tokens: nothing without positions, the roll-back alone with them."""
+    B, H, D = 2, 2, 64
+    f = Filled([50, 40], H, D, seed=4)
+    pos = torch.tensor([30, -1], dtype=torch.int32, device="cuda")
+    none, x, bits, table = cu_of([0] * B), rows(0, H, D, 1), widths(0, H, 1), rope_table(50, D)
+    q = rows(0, H, D, 2)
+    kvq.kvq_write_rope(q, x, x, bits, none, f.cache, table, positions=torch.full((B,), -1, dtype=torch.int32, device="cuda"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvq.kvq_write_rope(None, x, x, bits, none, f.cache, table)
+        out = kvq.kvq_write_rope(q, x, x, bits, none, f.cache, table, positions=pos)
+    assert out.shape == (0, H, D) and f.cache.lengths().tolist() == [50, 40]
+    graph.replay()
+    f.cache.check()
+    assert f.cache.lengths().tolist() == [30, 40]
+    pos.copy_(torch.tensor([29, 7], dtype=torch.int32))
+    graph.replay()
+    f.cache.check()
+    assert f.cache.lengths().tolist() == [29, 7]
