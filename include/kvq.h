@@ -230,7 +230,8 @@ int routed_attn_decode_noalloc(const void *q, const kvq_cache *cache, const uint
  *   rot_dim:   channels rotated, a multiple of 16 in [16, head_dim]; the others are copied.
  *   interleaved: 0: channel c is paired with c + rot_dim/2; 1: channel 2c with 2c + 1.
  *   positions: DEVICE int32 [batch] or NULL: roll each sequence back first, as in
- *              kvq_decode_step.
+ *              kvq_decode_step (a sequence whose range in cu_seqlens is inconsistent keeps its tokens,
+ *              KVQ_ERR_DEVICE_CHECK). With n_tok = 0 this is all the call does.
  *   q_out:     fp16 [n_tok][heads * query_group][head_dim], contiguous; may be q itself when
  *              q_stride is heads * query_group * head_dim.
  * Token i of sequence s sits at position t = (its KV head's length before the write) + i. A pair

@@ -49,13 +49,20 @@ int cuda_fail(cudaError_t e, const char *what)
     return fail(KVQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-__global__ void truncate_kernel(kvq::CacheView c, const int32_t *__restrict__ lengths)
+// cu (of a write of n_tok tokens that rolls back first) may be nullptr: a sequence whose range in it
+// is inconsistent is left alone.
+__global__ void truncate_kernel(kvq::CacheView c, const int32_t *__restrict__ lengths, const int32_t *__restrict__ cu,
+                                int64_t n_tok)
 {
     kvq::pdl_wait();
     kvq::pdl_trigger();
     const int sh = blockIdx.x * blockDim.x + threadIdx.x;
     if (sh >= c.B * c.H) return;
     const int s = sh / c.H, h = sh % c.H;
+    if (cu && (cu[s] < 0 || cu[s + 1] < cu[s] || cu[s + 1] > n_tok || (s == 0 && cu[0] != 0))) {
+        if (h == 0) kvq::set_status(c.status, KVQ_ERR_DEVICE_CHECK);
+        return;
+    }
     const int want = lengths[s];
     const int have = c.len[sh];
     if (want < 0 || want >= have) return;
@@ -129,10 +136,10 @@ bool valid_block(int block) { return block == 16 || block == 32 || block == 64 |
 } // namespace
 
 namespace kvq {
-cudaError_t launch_truncate(kvq_cache *c, const int32_t *lengths, cudaStream_t st)
+cudaError_t launch_truncate(kvq_cache *c, const int32_t *lengths, const int32_t *cu, int64_t n_tok, cudaStream_t st)
 {
     const int BH = c->B * c->H;
-    return launch_pdl(truncate_kernel, dim3((BH + 255) / 256), dim3(256), 0, st, c->view, lengths);
+    return launch_pdl(truncate_kernel, dim3((BH + 255) / 256), dim3(256), 0, st, c->view, lengths, cu, n_tok);
 }
 
 namespace {
@@ -457,7 +464,7 @@ int kvq_cache_truncate(kvq_cache *c, const int32_t *lengths, kvq_stream_t stream
 {
     if (!valid_cache(c)) return fail(KVQ_ERR_ARG, "kvq_cache_truncate: bad cache");
     if (!lengths) return fail(KVQ_ERR_ARG, "kvq_cache_truncate: lengths is NULL");
-    kvq::launch_truncate(c, lengths, reinterpret_cast<cudaStream_t>(stream));
+    kvq::launch_truncate(c, lengths, nullptr, 0, reinterpret_cast<cudaStream_t>(stream));
     cudaError_t e = cudaGetLastError();
     return e ? cuda_fail(e, "kvq_cache_truncate") : ok();
 }

@@ -399,8 +399,8 @@ cudaError_t launch_decode_step(kvq_cache *c, const __half *q, const __half *k, c
                                cudaStream_t st);
 cudaError_t launch_prefill_tc(const kvq_cache *c, const __half *q, const uint8_t *modes, int w,
                               const int32_t *cu, int64_t n_tok, float *out, cudaStream_t st);
-// rolls sequences back to `lengths` (kvq_cache_truncate)
-cudaError_t launch_truncate(kvq_cache *c, const int32_t *lengths, cudaStream_t st);
+// rolls sequences back to `lengths` (kvq_cache_truncate); with cu, those whose range in it is consistent
+cudaError_t launch_truncate(kvq_cache *c, const int32_t *lengths, const int32_t *cu, int64_t n_tok, cudaStream_t st);
 // SM count of the current device (cached per device ordinal)
 int num_sms();
 // Raise `func`'s dynamic shared-memory limit to `bytes` on the current device; done once

@@ -871,7 +871,7 @@ cudaError_t launch_write_rope(kvq_cache *cache, const __half *k, const __half *v
         profile_after(st);
         return le != cudaSuccess ? le : cudaGetLastError();
     }
-    if (positions && (le = launch_truncate(cache, positions, st)) != cudaSuccess) return le;
+    if (positions && (le = launch_truncate(cache, positions, cu, n_tok, st)) != cudaSuccess) return le;
     if (n_tok == 0) return cudaSuccess;
     profile_before(st);
     if ((le = launch_scan(cache, bits, cu, n_tok, gen, (int)std::min<int64_t>(r.max_pos, INT32_MAX), st)) != cudaSuccess)

@@ -101,3 +101,20 @@ def test_an_empty_write_is_captured():
     graph.replay()
     f.cache.check()
     assert f.cache.lengths().tolist() == [29, 7]
+
+
+@pytest.mark.parametrize("cu", [[0, 1, 2, 7], [0, 10, 20, 99], [0, 100, 200, 260], [0, 0, 0, 5]])
+def test_inconsistent_ranges_are_not_rolled_back(cu):
+    """Sequence 2's range ends behind the call's rows: it keeps its tokens, in every launch form."""
+    n = {7: 3, 99: 40, 260: 250, 5: 0}[cu[-1]]
+    B, H, D = 3, 2, 64
+    f = Filled([50, 40, 30], H, D, seed=4, capacity=[400] * B)
+    before = f.cache.export(2, 1, 0, 30)
+    pos = torch.tensor([20, 5, 10], dtype=torch.int32, device="cuda")
+    kvq.kvq_write_rope(None, rows(n, H, D, 1), rows(n, H, D, 2), widths(n, H, 3), torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                       f.cache, rope_table(400, D), positions=pos)
+    with pytest.raises(kvq.KVQError) as e:
+        f.cache.check()
+    assert e.value.code == kvq.KVQ_ERR_DEVICE_CHECK
+    assert f.cache.lengths().tolist() == [20 + cu[1] - cu[0], 5 + cu[2] - cu[1], 30]
+    assert all(torch.equal(a, b) for a, b in zip(f.cache.export(2, 1, 0, 30), before))
