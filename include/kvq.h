@@ -306,7 +306,7 @@ int kvq_select_blocks(const void *q, const kvq_cache *cache, const void *bounds,
  * ids[s][h] that the cache holds (its own key is among them when the last block is listed).
  *   ids:     int32 [batch][heads][k], 1 <= k <= KVQ_MAX_BLOCKS: ascending, then -1. An entry that is
  *            not above the one before it, or starts at or past the sequence's length, is passed
- *            over (KVQ_ERR_DEVICE_CHECK).
+ *            over (KVQ_ERR_DEVICE_CHECK). The list of a KV head without a full query is not read.
  *   block:   16, 32, 64 or 128; modes, w, out: as routed_attn_decode.
  *   scratch: DEVICE memory of the caller, 16-byte aligned, used by this call alone until it has
  *            run; at least routed_attn_decode_blocks_scratch() bytes (0 allows NULL). The scratch

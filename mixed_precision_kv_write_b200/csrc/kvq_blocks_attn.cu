@@ -459,7 +459,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
     // CTAs take equal shares, multiples of 32
     const int nb = (len + (1 << job.block_shift) - 1) >> job.block_shift;
     const int e_block = full ? ((min(job.k, nb) << job.block_shift) + 31) & ~31 : 0;
-    if (full && sub == 0 && split == 0)          // no list of distinct blocks is longer than nb
+    if (full && split == 0)                      // no list of distinct blocks is longer than nb
         for (int x = nb + tid; x < job.k; x += kThreads)
             if (job.ids[(int64_t)sh * job.k + x] >= 0) set_status(c.status, KVQ_ERR_DEVICE_CHECK);
     const int wl = min(len, (int)min((int64_t)job.w + 1, (int64_t)len));

@@ -118,3 +118,22 @@ def test_inconsistent_ranges_are_not_rolled_back(cu):
     assert e.value.code == kvq.KVQ_ERR_DEVICE_CHECK
     assert f.cache.lengths().tolist() == [20 + cu[1] - cu[0], 5 + cu[2] - cu[1], 30]
     assert all(torch.equal(a, b) for a, b in zip(f.cache.export(2, 1, 0, 30), before))
+
+
+# ------------------------------------------------------------------ attention over chosen blocks
+@pytest.mark.parametrize("G", [1, 4, 9, 20])
+@pytest.mark.parametrize("entry", [2, 30])                     # within the sequence's number of blocks, and behind it
+def test_bad_entries_are_reported_whichever_query_reads_them(G, entry):
+    f = Filled([100], 1, 64, G=G, seed=4)
+    ids = torch.full((1, 1, 40), -1, dtype=torch.int32, device="cuda")
+    ids[..., 0], ids[..., entry] = 1, 50                       # 7 blocks
+    q = rows(1, G, 64, 2)
+    for g in {0, G // 2, G - 1}:
+        modes = torch.zeros((1, G), dtype=torch.uint8, device="cuda")
+        modes[0, g] = 2
+        kvq.routed_attn_decode_blocks(q, f.cache, ids, 16, modes, 0)
+        with pytest.raises(kvq.KVQError) as e:
+            f.cache.check()
+        assert e.value.code == kvq.KVQ_ERR_DEVICE_CHECK
+    kvq.routed_attn_decode_blocks(q, f.cache, ids, 16, torch.ones((1, G), dtype=torch.uint8, device="cuda"), 3)
+    f.cache.check()                                            # no full query: the list is not read
