@@ -311,7 +311,8 @@ int kvq_select_blocks(const void *q, const kvq_cache *cache, const void *bounds,
  *   scratch: DEVICE memory of the caller, 16-byte aligned, used by this call alone until it has
  *            run; at least routed_attn_decode_blocks_scratch() bytes (0 allows NULL). The scratch
  *            function returns -1 for arguments the call would refuse.
- * A query whose blocks hold no key gets zeros.
+ * A query whose blocks hold no key gets zeros. Values that are not finite reach the queries that
+ * attend over their keys, and no others.
  */
 int64_t routed_attn_decode_blocks_scratch(const kvq_cache *cache, int k, int block, int w);
 int routed_attn_decode_blocks(const void *q, const kvq_cache *cache, const int32_t *ids, int k, int block,

@@ -499,175 +499,184 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
     }
     __syncthreads();
 
-    State<D> st;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        st.m[i] = kMInit;
-        st.l[i] = st.pz[i] = 0.f;
-        st.fac[i] = 1.f;
-    }
     Tile &tl = sm.tile;
     const RecLoc L = rec_loc(c, s, h, 0);
     const uint32_t *meta = c.meta + slot0;
     const float4 *side = c.side + slot0;
     const int bs = job.block_shift;
     const uint32_t below = (1u << lane) - 1u;
+    const bool cluster = job.n_split > 1 && job.n_split <= kMaxCluster;
     const int a0 = min(e_all, split * share), a1 = min(e_all, a0 + share);
-    for (int a = a0; a < a1;) {
-        // a tile: up to kTileKeys entries of one kind, the warps' parts multiples of 32
-        const bool blocks = a < e_block;
-        const int n = min(kTileKeys, (blocks ? min(a1, e_block) : a1) - a);
-        const int per = ((n + W - 1) / W + 31) & ~31;
-        const int p0 = warp * per, p1 = min(n, p0 + per);
-        const uint32_t act = blocks ? full : local;
-        // lane i < 17: the i-th block of the warp's part, or -1; an entry not above its predecessor
-        // or past the length is dropped
-        const int x0 = (a + p0) >> bs;
-        int id = -1;
-        if (blocks && p0 < p1) {
-            const int x = x0 + lane;
-            const bool in = x <= (a + p1 - 1) >> bs && x < job.k;
-            id = in ? job.ids[(int64_t)sh * job.k + x] : -1;
-            int before = __shfl_up_sync(0xffffffffu, id, 1);
-            if (lane == 0 && x > 0) before = job.ids[(int64_t)sh * job.k + x - 1];
-            if (id >= 0 && (id >= nb || (x > 0 && (before < 0 || id <= before)))) {
-                set_status(c.status, KVQ_ERR_DEVICE_CHECK);
-                id = -1;
+    // Where a unit has full and local queries, the blocks' keys are finished for the full ones before
+    // the window's begin for the others: a value that is not finite gives NaN in a column of weight 0.
+    const bool both = full && local;
+    for (int part = 0; part < (both ? 2 : 1); ++part) {
+        const int lo = part ? max(a0, e_block) : a0, hi = both && !part ? min(a1, e_block) : a1;
+        const uint32_t mine = !both ? 0xFFu : part ? ~full : full;       // the queries finished in this part
+        State<D> st;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            st.m[i] = kMInit;
+            st.l[i] = st.pz[i] = 0.f;
+            st.fac[i] = 1.f;
+        }
+        for (int a = lo; a < hi;) {
+            // a tile: up to kTileKeys entries of one kind, the warps' parts multiples of 32
+            const bool blocks = a < e_block;
+            const int n = min(kTileKeys, (blocks ? min(hi, e_block) : hi) - a);
+            const int per = ((n + W - 1) / W + 31) & ~31;
+            const int p0 = warp * per, p1 = min(n, p0 + per);
+            const uint32_t act = blocks ? full : local;
+            // lane i < 17: the i-th block of the warp's part, or -1; an entry not above its predecessor
+            // or past the length is dropped
+            const int x0 = (a + p0) >> bs;
+            int id = -1;
+            if (blocks && p0 < p1) {
+                const int x = x0 + lane;
+                const bool in = x <= (a + p1 - 1) >> bs && x < job.k;
+                id = in ? job.ids[(int64_t)sh * job.k + x] : -1;
+                int before = __shfl_up_sync(0xffffffffu, id, 1);
+                if (lane == 0 && x > 0) before = job.ids[(int64_t)sh * job.k + x - 1];
+                if (id >= 0 && (id >= nb || (x > 0 && (before < 0 || id <= before)))) {
+                    set_status(c.status, KVQ_ERR_DEVICE_CHECK);
+                    id = -1;
+                }
             }
-        }
-        uint32_t mt[kSteps];
-        int js[kSteps];
-        int cnt[4] = {0, 0, 0, 0};
+            uint32_t mt[kSteps];
+            int js[kSteps];
+            int cnt[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            mt[i] = 0u;
-            js[i] = 0;
-            if (p0 + i * 32 >= p1) continue;
-            const int e = a + p0 + i * 32 + lane;
-            const int b = __shfl_sync(0xffffffffu, id, (e >> bs) - x0);
-            js[i] = blocks ? (b << bs) + (e & ((1 << bs) - 1)) : len - wl + e - e_block;
-            if (e < a + p1 && (!blocks || b >= 0) && js[i] < len) mt[i] = meta[js[i]] | kValid;
-        }
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            if (p0 + i * 32 >= p1) continue;
-            const uint32_t v = __ballot_sync(0xffffffffu, mt[i] & kValid), b0 = __ballot_sync(0xffffffffu, mt[i] & 1u),
-                           b1 = __ballot_sync(0xffffffffu, mt[i] & 2u);
-            cnt[0] += __popc(v & ~b0 & ~b1);
-            cnt[1] += __popc(b0 & ~b1);
-            cnt[2] += __popc(b1 & ~b0);
-            cnt[3] += __popc(b0 & b1);
-        }
-        if (lane < 4) sm.cnt[warp][lane] = lane == 0 ? cnt[0] : lane == 1 ? cnt[1] : lane == 2 ? cnt[2] : cnt[3];
-        __syncthreads();
-        // slots: width by width, each width's keys in the warps' order, padded to 16. Lane
-        // 4 x + w holds warp x's count of width w; sums over the warps, then over the widths
-        int all[4], at[4], first[5];
-        {
-            const int mine = lane < 4 * W ? sm.cnt[lane >> 2][lane & 3] : 0;
-            int upto = mine;
-#pragma unroll
-            for (int d = 4; d < 4 * W; d <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, d);
-                if (lane >= d) upto += y;
+            for (int i = 0; i < kSteps; ++i) {
+                mt[i] = 0u;
+                js[i] = 0;
+                if (p0 + i * 32 >= p1) continue;
+                const int e = a + p0 + i * 32 + lane;
+                const int b = __shfl_sync(0xffffffffu, id, (e >> bs) - x0);
+                js[i] = blocks ? (b << bs) + (e & ((1 << bs) - 1)) : len - wl + e - e_block;
+                if (e < a + p1 && (!blocks || b >= 0) && js[i] < len) mt[i] = meta[js[i]] | kValid;
             }
-            first[0] = 0;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                if (p0 + i * 32 >= p1) continue;
+                const uint32_t v = __ballot_sync(0xffffffffu, mt[i] & kValid), b0 = __ballot_sync(0xffffffffu, mt[i] & 1u),
+                               b1 = __ballot_sync(0xffffffffu, mt[i] & 2u);
+                cnt[0] += __popc(v & ~b0 & ~b1);
+                cnt[1] += __popc(b0 & ~b1);
+                cnt[2] += __popc(b1 & ~b0);
+                cnt[3] += __popc(b0 & b1);
+            }
+            if (lane < 4) sm.cnt[warp][lane] = lane == 0 ? cnt[0] : lane == 1 ? cnt[1] : lane == 2 ? cnt[2] : cnt[3];
+            __syncthreads();
+            // slots: width by width, each width's keys in the warps' order, padded to 16. Lane
+            // 4 x + w holds warp x's count of width w; sums over the warps, then over the widths
+            int all[4], at[4], first[5];
+            {
+                const int my_cnt = lane < 4 * W ? sm.cnt[lane >> 2][lane & 3] : 0;
+                int upto = my_cnt;
+#pragma unroll
+                for (int d = 4; d < 4 * W; d <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, upto, d);
+                    if (lane >= d) upto += y;
+                }
+                first[0] = 0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    all[w] = __shfl_sync(0xffffffffu, upto, 4 * (W - 1) + w);
+                    at[w] = first[w] + __shfl_sync(0xffffffffu, upto - my_cnt, 4 * warp + w);
+                    first[w + 1] = first[w] + ((all[w] + 15) & ~15);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                if (p0 + i * 32 >= p1) continue;
+                const uint32_t v = __ballot_sync(0xffffffffu, mt[i] & kValid), b0 = __ballot_sync(0xffffffffu, mt[i] & 1u),
+                               b1 = __ballot_sync(0xffffffffu, mt[i] & 2u);
+                if (mt[i] & kValid) {
+                    const uint32_t own = v & (mt[i] & 1u ? b0 : ~b0) & (mt[i] & 2u ? b1 : ~b1);
+                    const int to = mt[i] & 2u ? (mt[i] & 1u ? at[3] : at[2]) : (mt[i] & 1u ? at[1] : at[0]);
+                    const int end = mt[i] & 2u ? (mt[i] & 1u ? first[3] + all[3] : first[2] + all[2])
+                                               : (mt[i] & 1u ? first[1] + all[1] : all[0]);
+                    int pos = to + __popc(own & below);
+                    tl.ent[pos] = make_uint2(mt[i], (uint32_t)js[i]);
+                    // the width's last key also fills its last 16, without kValid
+                    if (++pos == end)
+                        for (; pos & 15; ++pos) tl.ent[pos] = make_uint2(mt[i] & ~kValid, (uint32_t)js[i]);
+                }
+                at[0] += __popc(v & ~b0 & ~b1);
+                at[1] += __popc(b0 & ~b1);
+                at[2] += __popc(b1 & ~b0);
+                at[3] += __popc(b0 & b1);
+            }
+            __syncthreads();
+            const bool on0 = (act >> (2 * t & (NQ - 1))) & 1u, on1 = (act >> ((2 * t & (NQ - 1)) + 1)) & 1u;
+            // 16-key steps dealt to the warps in turn, so that they run one width's code at a time
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                all[w] = __shfl_sync(0xffffffffu, upto, 4 * (W - 1) + w);
-                at[w] = first[w] + __shfl_sync(0xffffffffu, upto - mine, 4 * warp + w);
-                first[w + 1] = first[w] + ((all[w] + 15) & ~15);
+                const int b0 = first[w] + ((warp - first[w] / 16) & (W - 1)) * 16, b1 = first[w + 1];
+                if (b0 >= b1) continue;
+                if (w == 0) run_class<D, 0, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
+                else if (w == 1) run_class<D, 1, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
+                else if (w == 2) run_class<D, 2, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
+                else run_class<D, 3, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
+            }
+            a += n;
+            __syncthreads();                         // the tile's slots are read; the next one overwrites them
+        }
+
+        // this warp's sums over its lanes, then the warps' states through shared memory
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], d);
+                st.pz[i] += __shfl_xor_sync(0xffffffffu, st.pz[i], d);
             }
         }
+        // columns 4..7 of up to 4 queries are the weights' second parts: left as states of their own
+        if (2 * (t & (NQ / 2 - 1)) < nq) {
+            const int g = lane >> 2;
+            const bool rest = 2 * t >= NQ;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            if (p0 + i * 32 >= p1) continue;
-            const uint32_t v = __ballot_sync(0xffffffffu, mt[i] & kValid), b0 = __ballot_sync(0xffffffffu, mt[i] & 1u),
-                           b1 = __ballot_sync(0xffffffffu, mt[i] & 2u);
-            if (mt[i] & kValid) {
-                const uint32_t own = v & (mt[i] & 1u ? b0 : ~b0) & (mt[i] & 2u ? b1 : ~b1);
-                const int to = mt[i] & 2u ? (mt[i] & 1u ? at[3] : at[2]) : (mt[i] & 1u ? at[1] : at[0]);
-                const int end = mt[i] & 2u ? (mt[i] & 1u ? first[3] + all[3] : first[2] + all[2])
-                                           : (mt[i] & 1u ? first[1] + all[1] : all[0]);
-                int pos = to + __popc(own & below);
-                tl.ent[pos] = make_uint2(mt[i], (uint32_t)js[i]);
-                // the width's last key also fills its last 16, without kValid
-                if (++pos == end)
-                    for (; pos & 15; ++pos) tl.ent[pos] = make_uint2(mt[i] & ~kValid, (uint32_t)js[i]);
+            for (int i = 0; i < 2; ++i) {
+                float *o = sm.o[warp][2 * t + i];
+                const float add = rest ? 0.f : st.pz[i], unit = __uint_as_float((254u << 23) - __float_as_uint(st.fac[i]));
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt)
+                    *reinterpret_cast<float2 *>(&o[g * (D / 8) + 2 * mt]) =
+                        make_float2(fmaf(st.o[mt][i], unit, add), fmaf(st.o[mt][2 + i], unit, add));
+                if (g == 0 && !rest) {
+                    o[D] = st.m[i];
+                    o[D + 1] = st.l[i];
+                }
             }
-            at[0] += __popc(v & ~b0 & ~b1);
-            at[1] += __popc(b0 & ~b1);
-            at[2] += __popc(b1 & ~b0);
-            at[3] += __popc(b0 & b1);
         }
         __syncthreads();
-        const bool on0 = (act >> (2 * t & (NQ - 1))) & 1u, on1 = (act >> ((2 * t & (NQ - 1)) + 1)) & 1u;
-        // 16-key steps dealt to the warps in turn, so that they run one width's code at a time
+        for (int x = tid; x < nq * D; x += kThreads) {
+            const int qi = x / D, ch = x % D;
+            if (!(mine >> qi & 1u)) continue;
+            float M = kMInit, l = 0.f, o = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int b0 = first[w] + ((warp - first[w] / 16) & (W - 1)) * 16, b1 = first[w + 1];
-            if (b0 >= b1) continue;
-            if (w == 0) run_class<D, 0, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
-            else if (w == 1) run_class<D, 1, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
-            else if (w == 2) run_class<D, 2, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
-            else run_class<D, 3, PAGED, NQ, W>(st, sm, L, side, b0, b1, on0, on1);
-        }
-        a += n;
-        __syncthreads();                         // the tile's slots are read; the next one overwrites them
-    }
-
-    // this warp's sums over its lanes, then the warps' states through shared memory
+            for (int wp = 0; wp < W; ++wp) M = fmaxf(M, sm.o[wp][qi][D]);
 #pragma unroll
-    for (int d = 4; d < 32; d <<= 1) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], d);
-            st.pz[i] += __shfl_xor_sync(0xffffffffu, st.pz[i], d);
-        }
-    }
-    // columns 4..7 of up to 4 queries are the weights' second parts: left as states of their own
-    if (2 * (t & (NQ / 2 - 1)) < nq) {
-        const int g = lane >> 2;
-        const bool rest = 2 * t >= NQ;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float *o = sm.o[warp][2 * t + i];
-            const float add = rest ? 0.f : st.pz[i], unit = __uint_as_float((254u << 23) - __float_as_uint(st.fac[i]));
-#pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt)
-                *reinterpret_cast<float2 *>(&o[g * (D / 8) + 2 * mt]) =
-                    make_float2(fmaf(st.o[mt][i], unit, add), fmaf(st.o[mt][2 + i], unit, add));
-            if (g == 0 && !rest) {
-                o[D] = st.m[i];
-                o[D + 1] = st.l[i];
+            for (int wp = 0; wp < W; ++wp) {
+                const float f = ex2(sm.o[wp][qi][D] - M);
+                l = fmaf(sm.o[wp][qi][D + 1], f, l);
+                o = fmaf(sm.o[wp][qi][ch] + (NQ == 4 ? sm.o[wp][qi + 4][ch] : 0.f), f, o);
+            }
+            if (job.n_split == 1) {
+                out[(q0 + qi) * D + ch] = l == 0.f ? 0.f : o / l;
+                continue;
+            }
+            float *to = cluster ? sm.done[qi] : job.part + (((int64_t)unit * job.n_split + split) * job.qs + qi) * (D + 4);
+            to[ch] = o;
+            if (ch == 0) {
+                to[D] = M;
+                to[D + 1] = l;
             }
         }
-    }
-    __syncthreads();
-    const bool cluster = job.n_split > 1 && job.n_split <= kMaxCluster;
-    for (int x = tid; x < nq * D; x += kThreads) {
-        const int qi = x / D, ch = x % D;
-        float M = kMInit, l = 0.f, o = 0.f;
-#pragma unroll
-        for (int wp = 0; wp < W; ++wp) M = fmaxf(M, sm.o[wp][qi][D]);
-#pragma unroll
-        for (int wp = 0; wp < W; ++wp) {
-            const float f = ex2(sm.o[wp][qi][D] - M);
-            l = fmaf(sm.o[wp][qi][D + 1], f, l);
-            o = fmaf(sm.o[wp][qi][ch] + (NQ == 4 ? sm.o[wp][qi + 4][ch] : 0.f), f, o);
-        }
-        if (job.n_split == 1) {
-            out[(q0 + qi) * D + ch] = l > 0.f ? o / l : 0.f;
-            continue;
-        }
-        float *p = cluster ? sm.done[qi] : job.part + (((int64_t)unit * job.n_split + split) * job.qs + qi) * (D + 4);
-        p[ch] = o;
-        if (ch == 0) {
-            p[D] = M;
-            p[D + 1] = l;
-        }
+        if (both) __syncthreads();                   // the states are read; the next part's tile overwrites them
     }
     if (!cluster) return;
     // the cluster's CTAs share the outputs; each reads every CTA's state
@@ -689,7 +698,7 @@ decode_blocks_kernel(CacheView c, const __half *__restrict__ q, Job job, float *
             l = fmaf(cl.map_shared_rank(&sm.done[qi][D + 1], r)[0], f, l);
             o = fmaf(cl.map_shared_rank(&sm.done[qi][ch], r)[0], f, o);
         }
-        out[(q0 + qi) * D + ch] = l > 0.f ? o / l : 0.f;
+        out[(q0 + qi) * D + ch] = l == 0.f ? 0.f : o / l;
     }
     cl.sync();                                   // every CTA's state has been read
 }
@@ -721,7 +730,7 @@ decode_blocks_combine_kernel(Job job, int64_t n_out, int G, int nq, float *__res
         for (int e = 0; e < N; ++e) o[e] = fmaf(p[i * step + lane + 32 * e], f, o[e]);
     }
 #pragma unroll
-    for (int e = 0; e < N; ++e) out[hq * D + lane + 32 * e] = l > 0.f ? o[e] / l : 0.f;
+    for (int e = 0; e < N; ++e) out[hq * D + lane + 32 * e] = l == 0.f ? 0.f : o[e] / l;
 }
 
 int shift_of(int block)
