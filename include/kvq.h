@@ -264,7 +264,8 @@ int kvq_read(const kvq_cache *cache, const int32_t *cu_seqlens, int64_t n_rows, 
 /*
  * Bounds of blocks of `block` (16, 32, 64 or 128) consecutive keys of each (sequence, KV
  * head): per channel the minimum and the maximum of deq(k_j) over the block's keys, rounded
- * to fp16 (no counterpart in the paper: the index that kvq_select_blocks reads).
+ * to fp16, a NaN among them making both NaN (no counterpart in the paper: the index that
+ * kvq_select_blocks reads).
  *   cu_seqlens: NULL: every block that holds a key. Else int32 [batch + 1]: only the blocks that
  *               hold one of the last cu_seqlens[s+1] - cu_seqlens[s] tokens of sequence s (each
  *               from its first key on), and of a sequence without new tokens its last block when
@@ -293,7 +294,8 @@ int kvq_block_bounds(const kvq_cache *cache, int block, const int32_t *cu_seqlen
  *   k:      1 .. KVQ_MAX_BLOCKS. The first `first` and last `last` blocks of the sequence are
  *           always chosen (first + last <= k); the others by score, ties to the lower index.
  *   scores: fp32 [batch][heads][nt][64], 16-byte aligned: every block's score (the sum is
- *           taken in fp64 and rounded once), -inf past the last block and without a full query.
+ *           taken in fp64 and rounded once), -inf past the last block and without a full query. A
+ *           query's sum that is not a number counts as -inf.
  *   ids:    int32 [batch][heads][k]: the chosen blocks in ascending order, then -1.
  */
 int kvq_select_blocks(const void *q, const kvq_cache *cache, const void *bounds, int block,

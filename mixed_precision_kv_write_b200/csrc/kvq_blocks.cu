@@ -39,7 +39,7 @@ struct BoundsSmem {
     uint4 ent[W][kMaxRun];                               // a run's keys by width: offset, s, z
 };
 
-// lo and hi over the n keys of `ent`, all of width 2 << CLS; gk, li: the lane's key of a step and
+// lo and hi (a NaN stays one) over the n keys of `ent`, all of width 2 << CLS; gk, li: the lane's key of a step and
 // its 16 channels. A last step's missing keys repeat the last one, which changes nothing.
 template <int D, int CLS, bool PAGED>
 __device__ __forceinline__ void bounds_class(__half2 (&lo)[8], __half2 (&hi)[8], const RecLoc &L, const uint4 *ent, int n, int gk,
@@ -98,8 +98,8 @@ __device__ __forceinline__ void bounds_class(__half2 (&lo)[8], __half2 (&hi)[8],
                                                 make_float2(z, z));
                     x = __floats2half2_rn(y.x, y.y);
                 }
-                lo[e / 2] = __hmin2(lo[e / 2], x);
-                hi[e / 2] = __hmax2(hi[e / 2], x);
+                lo[e / 2] = __hmin2_nan(lo[e / 2], x);
+                hi[e / 2] = __hmax2_nan(hi[e / 2], x);
             }
         }
     }
@@ -205,8 +205,8 @@ bounds_kernel(CacheView c, int block, const int32_t *__restrict__ cu, __half *__
             for (int d = LPK; d < 32; d <<= 1) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    lo[e] = __hmin2(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
-                    hi[e] = __hmax2(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
+                    lo[e] = __hmin2_nan(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], d));
+                    hi[e] = __hmax2_nan(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], d));
                 }
             }
             if (gk == 0) {
@@ -239,7 +239,7 @@ bounds_kernel(CacheView c, int block, const int32_t *__restrict__ cu, __half *__
                 const int b = b0 + t / (2 * D), mc = t % (2 * D);               // mc: [lo/hi][channel]
                 const __half *p = &sm.part[(b - b0) * subs][mc];
                 __half r = p[0];
-                for (int q = 1; q < subs; ++q) r = mc < D ? __hmin(r, p[q * (2 * D + 2)]) : __hmax(r, p[q * (2 * D + 2)]);
+                for (int q = 1; q < subs; ++q) r = mc < D ? __hmin_nan(r, p[q * (2 * D + 2)]) : __hmax_nan(r, p[q * (2 * D + 2)]);
                 bounds[(((int64_t)sh * nt + b / kTile) * 2 * D + mc) * kTile + b % kTile] = __hadd(r, __ushort_as_half(0));
             }
         }
@@ -254,7 +254,8 @@ bounds_kernel(CacheView c, int block, const int32_t *__restrict__ cu, __half *__
 // fp32 score is the correctly rounded one but for ties that close. fp16 -> fp64 takes one
 // shift and one mask: the fp16 bits moved to the same field of a double (sign, exponent at
 // bit 52 on) are the value times 2^-1008, subnormals included (fp64 arithmetic keeps them).
-// q carries 2^1000, the score 2^8. Bound by the latency of its one pass: 1024 heads x 128 blocks
+// q carries 2^1000, the score 2^8. Bounds that are not finite have no such form: a warp that has met
+// one (the largest magnitude of its loads says so) takes its tile's sums again, by conversions. Bound by the latency of its one pass: 1024 heads x 128 blocks
 // (33.5 MB of bounds) are scored and chosen in 14.5 us.
 constexpr int kSThreads = 128, kSWarps = kSThreads / 32;
 constexpr double kQUp = 1.0715086071862673e301;                // 2^1000
@@ -262,6 +263,11 @@ constexpr double kQUp = 1.0715086071862673e301;                // 2^1000
 __device__ __forceinline__ double half_field(uint32_t top)     // the fp16 bits in bits 16..31 of `top`
 {
     return __hiloint2double((int)((uint32_t)((int32_t)top >> 6) & 0x81FFFC00u), 0);
+}
+
+__device__ __forceinline__ double half_value(uint32_t top)     // the same for every value
+{
+    return (double)__half2float(__ushort_as_half((unsigned short)(top >> 16))) * (1.0 / (kQUp * 256.0));
 }
 
 // The scores of tiles [t0, t1) of 64 blocks of one (sequence, KV head), by a CTA. Two tiles at a
@@ -318,6 +324,7 @@ __device__ __forceinline__ void score_tiles(const CacheView &c, const __half *__
             for (int g = 0; g < NQ; ++g)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[g][e] = 0.0;
+            __half2 top = __half2half2(__ushort_as_half(0));   // the largest magnitude met
             if (some) {
 #pragma unroll(NQ == 1 ? 8 : NQ == 2 ? 4 : 2)
                 for (int ch = w0 * 4 + sub; ch < D; ch += 4 * wpt) {
@@ -330,6 +337,11 @@ __device__ __forceinline__ void score_tiles(const CacheView &c, const __half *__
                     }
                     const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __half2 *>(&uw[e])));
+                        if (NQ > 1) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __half2 *>(&lw[e])));
+                    }
+#pragma unroll
                     for (int g = 0; g < NQ; ++g) {
                         const double qv = sm.qs[g][ch];
 #pragma unroll
@@ -337,6 +349,29 @@ __device__ __forceinline__ void score_tiles(const CacheView &c, const __half *__
                             const uint32_t w = NQ == 1 ? uw[e] : (qv < 0.0 ? lw[e] : uw[e]);
                             acc[g][2 * e] = fma(qv, half_field(w << 16), acc[g][2 * e]);
                             acc[g][2 * e + 1] = fma(qv, half_field(w), acc[g][2 * e + 1]);
+                        }
+                    }
+                }
+            }
+            const bool odd = __hisnan(__hmul(__low2half(top), __ushort_as_half(0))) ||
+                             __hisnan(__hmul(__high2half(top), __ushort_as_half(0)));
+            if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+                for (int g = 0; g < NQ; ++g)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[g][e] = 0.0;
+#pragma unroll 1
+                for (int ch = w0 * 4 + sub; ch < D; ch += 4 * wpt) {
+                    const uint4 l = __ldg(lo + ch * (kTile / 8) + b8), u = __ldg(hi + ch * (kTile / 8) + b8);
+                    const uint32_t lw[4] = {l.x, l.y, l.z, l.w}, uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int g = 0; g < NQ; ++g) {
+                        const double qv = sm.qs[g][ch];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t w = qv < 0.0 ? lw[e] : uw[e];
+                            acc[g][2 * e] = fma(qv, half_value(w << 16), acc[g][2 * e]);
+                            acc[g][2 * e + 1] = fma(qv, half_value(w), acc[g][2 * e + 1]);
                         }
                     }
                 }

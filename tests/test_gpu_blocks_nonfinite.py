@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from blocks_testlib import Filled, assert_attention, attention64, rows
+from blocks_testlib import Filled, assert_attention, attention64, cu_of, flat_bounds, rows
 from mixed_precision_kv_write_b200 import kvq
 
 pytestmark = pytest.mark.gpu
@@ -104,3 +104,72 @@ def test_no_keys_is_still_zero():
     got = kvq.routed_attn_decode_blocks(rows(1, 2, 64, 1), f.cache, ids, 16, torch.tensor([[2, 0]], dtype=torch.uint8,
                                                                                          device="cuda"), 0)
     assert bool((got == 0).all())
+
+
+# ------------------------------------------------------------------ bounds and choice
+@pytest.mark.parametrize("block,new", [(16, None), (64, None), (128, None), (16, 1), (64, 70), (128, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bounds_of_keys_that_are_not_finite(block, new, D):
+    """Infinite keys bound their channel, a NaN makes both bounds NaN; the other blocks are as ever."""
+    lens, H = [700, 129], 2
+    f = Filled([0, 0], H, D, seed=1, capacity=lens)
+    g = Filled(lens, H, D, seed=1)
+    k, bits = g.k, g.bits
+    for i, (at, b, x) in enumerate([(3, 16, INF), (40, 16, -INF), (41, 16, INF), (200, 4, INF), (333, 16, NAN), (690, 16, -INF),
+                                    (699, 2, -INF), (699 + 100, 16, NAN), (699 + 129, 16, INF)]):
+        k[at, i % H, 7 * i], bits[at] = x, b
+    kvq.kvq_write(k, g.v, bits, g.cu, f.cache)
+    bounds = kvq.block_bounds(f.cache, block)
+    if new is not None:
+        fresh, cu = bounds, torch.tensor([0, new, 2 * new], dtype=torch.int32, device="cuda")
+        bounds = kvq.block_bounds(f.cache, block, cu, out=fresh.clone())
+    f.cache.check()
+    held, _ = kvq.kvq_read(f.cache, g.cu, g.start[-1], torch.float32)
+    fb = flat_bounds(bounds)
+    for s, L in enumerate(lens):
+        x = held[g.start[s]:g.start[s] + L].half()
+        for n in range(-(-L // block)):
+            part = x[n * block:(n + 1) * block]
+            assert torch.equal(fb[s, :, 0, :, n].isnan(), part.isnan().any(0))
+            for i, pick in enumerate(("amin", "amax")):
+                assert torch.equal(fb[s, :, i, :, n].nan_to_num(9.0, INF, -INF),
+                                   getattr(part, pick)(0).nan_to_num(9.0, INF, -INF))
+
+
+@pytest.mark.parametrize("L,G,D,block", [(700, 1, 64, 16), (700, 2, 128, 16), (9000, 4, 64, 32), (9000, 1, 128, 64),
+                                         (70000, 3, 64, 16)])
+def test_choice_with_bounds_that_are_not_finite(L, G, D, block):
+    """Scores in 64 bits with IEEE rules; a sum that is not a number counts as -inf."""
+    B, H, k = 2, 2, 9
+    cache = kvq.KVQCache(B, H, D, L, query_group=G)
+    x = torch.zeros((B * L, H, D), dtype=torch.float16, device="cuda")
+    kvq.kvq_write(x, x, torch.full((B * L, H), 2, dtype=torch.uint8, device="cuda"), cu_of([L] * B), cache)
+    nt, nb = kvq.block_tiles(cache, block), -(-L // block)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    mid = torch.randn((B, H, nt, 1, D, 64), generator=g, device="cuda")
+    b = torch.cat((mid - 2, mid + 2), 3).half()
+    u = torch.rand(b.shape, generator=g, device="cuda")
+    lo, hi = b[:, :, :, 0], b[:, :, :, 1]
+    lo[u[:, :, :, 0] < 0.3 / D] = -INF
+    hi[u[:, :, :, 1] < 0.3 / D] = INF
+    both = u[:, :, :, 0] > 1 - 0.1 / D                         # a NaN key's channel
+    lo[both], hi[both] = NAN, NAN
+    same = u[:, :, :, 1] > 1 - 0.1 / D                         # every key of the block the same infinity
+    lo[same], hi[same] = -INF, -INF
+    q = rows(B, H * G, D, 3)
+    q[q == 0] = 1.0
+    ids, scores = kvq.select_blocks(q, cache, b, block, k, first=0, last=0)
+    cache.check()
+    fb, qd = flat_bounds(b).double(), q.double().view(B, H, G, D, 1)
+    ref = torch.where(qd < 0, qd * fb[:, :, None, 0], qd * fb[:, :, None, 1]).sum(3).nan_to_num(-INF, INF, -INF).amax(2)
+    ref[..., nb:] = -INF
+    got = scores.double()
+    odd = ~ref.isfinite()
+    assert torch.equal(got[odd], ref[odd]) and bool((ref[..., :nb] == INF).any()) and bool((ref[..., :nb] == -INF).any())
+    mag = float(q.double().abs().sum(-1).max()) * 8
+    assert bool(((got - ref)[~odd].abs() <= 2.0 ** -24 * ref[~odd].abs() + D * 2.0 ** -52 * mag).all())
+    for s in range(B):                                         # by score, ties to the lower index
+        for h in range(H):
+            row = scores[s, h, :nb].tolist()
+            want = sorted(sorted(range(nb), key=lambda n: (-row[n], n))[:k])
+            assert ids[s, h].tolist() == want
