@@ -305,7 +305,7 @@ def _rows(t, name, heads, head_dim, device, n=None):
         shape, st = t.shape, t.stride()
         if len(shape) == 3 and shape[1] == heads and shape[2] == head_dim and (n is None or shape[0] == n) and \
                 st[2] == 1 and (st[1] == head_dim or heads == 1):
-            return st[0] if shape[0] > 1 else max(st[0], heads * head_dim)
+            return st[0] if shape[0] > 1 else heads * head_dim       # (the stride of a single row says nothing)
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:

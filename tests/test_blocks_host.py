@@ -36,3 +36,13 @@ def test_tiles_of_the_bounds(capacity, block, tiles):
 def test_other_blocks_are_refused(block):
     with pytest.raises(ValueError):
         kvq.block_tiles(types.SimpleNamespace(capacity=[100]), block)
+
+
+@pytest.mark.parametrize("heads,stride,n,want", [(2, 128, 3, 128), (2, 400, 3, 400), (1, 72, 5, 72), (2, 404, 1, 128),
+                                                 (2, 7, 1, 128), (2, 0, 1, 128), (1, 1, 0, 64), (3, 193, 0, 192)])
+def test_row_strides(heads, stride, n, want):
+    """The stride of several rows is theirs; that of one row or none, which nothing reads, the row's size."""
+    import torch
+    flat = torch.zeros(3000, dtype=torch.float16)
+    x = flat.as_strided((n, heads, 64), (stride, 64, 1))
+    assert kvq._rows(x, "k", heads, 64, flat.device) == want

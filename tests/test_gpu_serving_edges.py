@@ -137,3 +137,20 @@ def test_bad_entries_are_reported_whichever_query_reads_them(G, entry):
         assert e.value.code == kvq.KVQ_ERR_DEVICE_CHECK
     kvq.routed_attn_decode_blocks(q, f.cache, ids, 16, torch.ones((1, G), dtype=torch.uint8, device="cuda"), 3)
     f.cache.check()                                            # no full query: the list is not read
+
+
+@pytest.mark.parametrize("width", [521, 520])
+def test_one_row_of_a_projection_of_any_width(width):
+    """A single token's q, k and v as column ranges of one row: its stride does not matter."""
+    H, G, D = 1, 2, 128
+    f, plain = (Filled([3], H, D, G=G, seed=1, capacity=[9]) for _ in range(2))
+    x = rows(1, 1, width, 2).flatten().as_strided((1, G + 2, D), (width, D, 1))
+    q, k, v = x[:, :G], x[:, G:G + 1], x[:, G + 1:]
+    assert x.stride(0) == width
+    table, bits = rope_table(9, D), widths(1, H, 1)
+    out = kvq.kvq_write_rope(q, k, v, bits, cu_of([1]), f.cache, table)
+    want = kvq.kvq_write_rope(*(t.clone(memory_format=torch.contiguous_format) for t in (q, k, v)), bits, cu_of([1]),
+                              plain.cache, table)
+    f.cache.check()
+    assert torch.equal(out, want)
+    assert all(torch.equal(a, b) for a, b in zip(f.cache.export(0, 0, 0, 4), plain.cache.export(0, 0, 0, 4)))
