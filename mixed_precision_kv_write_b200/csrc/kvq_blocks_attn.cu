@@ -745,10 +745,19 @@ int shift_of(int block)
 int queries_per_warp(int G) { return G <= 4 ? 4 : kQ; }
 int subgroups(int G) { return (G + queries_per_warp(G) - 1) / queries_per_warp(G); }
 
-// Warps per CTA and CTAs per (sequence, KV head, subgroup). A CTA per unit, of 4 warps, when
-// that gives every SM four of them; else 8 warps, and enough CTAs for two an SM with at least
-// 64 keys a warp. (Batch 64, 16 heads: 62 us with 4 warps, 67 with 8, 74 with 2 CTAs a unit;
-// 20 units of 4096 keys: 17 us with 8 warps, 20.5 with 4.)
+// Warps per CTA and CTAs per (sequence, KV head, subgroup), a unit. An SM holds two CTAs of 8 warps
+// or four of 4. Up to 2.5 units an SM: 8 warps, and as many CTAs a unit as one wave takes, with at
+// least 64 keys a warp; above: a CTA of 4 warps a unit. Measured from cold caches, 1024 keys a full
+// query, 513 a local one, us for 4 warps x 1 CTA, 8 x 1, 8 x 2 (first every query full, then 15 %
+// skip, 45 % local; G = 1, D = 128):
+//   144 units   38.9  28.7  24.6     37.2  26.6  23.9
+//   256         43.0  32.8  43.0     41.0  30.7  38.9
+//   320         47.1  51.2  58.9     43.0  33.0  41.0
+//   384         49.1  54.8  61.5     43.9  43.2  49.2
+//   512         53.3  59.4  77.9     49.2  49.6  61.5
+//   640         83.3  77.4  94.8     51.2  55.3  72.0
+//   1024        95.3 103.6 131.2     78.4  79.9 107.8
+// (4 queries a head: 256 units 43.8 34.8 45.1 | 61.5 47.1 58.5, 512 units 55.3 61.4 82.2 | 75.8 84.9 99.9.)
 struct Shape {
     int warps, n_split;
 };
@@ -756,12 +765,11 @@ Shape shape_of(const kvq_cache *cache, int k, int block, int w)
 {
     const CacheView &c = cache->view;
     const int64_t units = (int64_t)c.B * c.H * subgroups(c.G), sms = num_sms();
-    if (units >= 4 * sms) return {4, 1};
+    if (2 * units >= 5 * sms) return {4, 1};
     const int64_t keys_b = std::min<int64_t>((int64_t)k * block, ((int64_t)cache->max_cap + block - 1) / block * block);
     const int64_t keys_w = std::min<int64_t>((int64_t)w + 1, cache->max_cap);
     const int64_t keys = c.G == 1 ? std::max(keys_b, keys_w) : keys_b + keys_w;
-    const int64_t want = (2 * sms + units - 1) / units;
-    return {8, (int)std::max<int64_t>(1, std::min<int64_t>(want, (keys + 64 * 8 - 1) / (64 * 8)))};
+    return {8, (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms / units, (keys + 64 * 8 - 1) / (64 * 8)))};
 }
 
 template <int D, bool PAGED, int NQ, int W>
