@@ -30,6 +30,8 @@
  *     error in the cache's device status word, and kvq_check() reports it.
  *   - Calls that touch one cache must be ordered (same stream, or events); the cache
  *     holds per-call scratch, so two calls on one cache that overlap on the GPU race.
+ *     kvq_read, kvq_block_bounds, kvq_select_blocks and routed_attn_decode_blocks keep
+ *     nothing in it: they may overlap with one another, each with buffers of its own.
  */
 #ifndef KVQ_H
 #define KVQ_H

@@ -9,7 +9,7 @@
 // fp16) and z' = z + (2^b - 1)/2 s:
 //   q . deq(k_j) = s_j (q . c'_j) + z'_j sum(q),   sum_j p_j deq(v_j) = sum_j (p_j s_j) c'_j + sum_j p_j z'_j
 // Centring keeps the sums from cancelling: with K's codes as they are (a mask alone makes a field an
-// fp16 subnormal, two instructions less a pair) the outputs were 9e-6 off, with centred ones 3e-7 to 6e-7.
+// fp16 subnormal, two instructions less a pair) the outputs were 9e-6 off, with centred ones 2e-7 to 6e-7.
 //
 // One warp serves up to 8 query heads of a KV head at once with m16n8k16 matrix
 // instructions (fp16 operands, fp32 sums), 16 keys at a time:
@@ -41,8 +41,9 @@
 // distributed shared memory; more of them leave partial states in the caller's scratch, which
 // a second launch merges.
 //
-// Bound by its instructions at 16 warps an SM (the state of 8 columns x D channels takes the
-// registers): 656 k keys of 1024 heads take 65 us, 38 warp instructions a key, 2.0 TB/s of records.
+// Bound by latency at 16 warps an SM (the state of 8 columns x D channels takes the registers):
+// 656 k keys of 1024 heads take 66 us, 37 warp instructions a key, 2.0 TB/s of records. At 42 %
+// issue-active and 23 % of DRAM's rate neither is a limit; the wait for a step's records is the top stall.
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -640,7 +640,8 @@ __device__ __forceinline__ void rope_q_tile(const CacheView &c, const RopeArgs &
 // cu_seqlens), the call's verdict, the write start, and the record offset the scan kernel
 // assigned. Then each vector of D values is quantized by one lane from shared memory.
 // ROPE: rows have the strides of `r`; the staged K rows are rotated before they are
-// quantized, and the CTAs beyond the n_tiles, which come first, rotate the call's query rows.
+// quantized. The grid has n_tiles CTAs for the K and V tiles and, before them, those that rotate
+// the call's query rows.
 template <int D, bool ROPE>
 __device__ __forceinline__ void write_quant_body(const CacheView &c, const __half *__restrict__ k,
                                                  const __half *__restrict__ v, const int32_t *__restrict__ cu,

@@ -2,8 +2,10 @@
 
 Argument marshalling only: every step of the write and attention paths runs in the CUDA
 library. Tensors must be CUDA tensors on the cache's device; the current torch stream is
-passed to every call unless `stream` is given. There is no CPU fallback: if the library is
-missing or a tensor is on the CPU, the call raises.
+passed to every call unless `stream` is given. With `stream`, tensors that the call makes are
+that stream's memory; the order of the two streams (inputs before the call, results after
+it) is the caller's. There is no CPU fallback: if the library is missing or a tensor is on the
+CPU, the call raises.
 """
 from __future__ import annotations
 
